@@ -14,6 +14,7 @@ PARK_ERR_WORKSPACE = 3
 PARK_ERR_CUDA = 4
 PARK_ERR_RANGE = 5
 PARK_ERR_TIMEOUT = 6
+PARK_ERR_INDEX = 7
 
 PARK_BF16 = 0
 PARK_F32 = 1
@@ -42,7 +43,9 @@ PARK_NUM_COUNTERS = 8
 # Every symbol include/park.h declares (checked by the CPU tests).
 EXPORTS = ("park_workspace_size", "park_retrieve", "park_sparse_attn", "park_layer", "park_status_string",
            "park_launch_count", "park_version", "park_profile_enable", "park_profile_collect",
-           "park_qrkc_metric_static", "park_set_wait_limit_ns")
+           "park_qrkc_metric_static", "park_set_wait_limit_ns", "park_rope_table_floats", "park_rope_table",
+           "park_rope", "park_qk_norm_rope", "park_qk_norm_rope_bwd_workspace", "park_qk_norm_rope_bwd",
+           "park_attention_workspace", "park_attention", "park_attention_bwd")
 
 
 class ParkShape(ctypes.Structure):
@@ -67,6 +70,22 @@ class ParkRetrieval(ctypes.Structure):
 
 class ParkKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("total_ms", ctypes.c_double), ("launches", ctypes.c_int64)]
+
+
+class ParkOperand(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("H", ctypes.c_int), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64),
+                ("sn", ctypes.c_int64)]
+
+
+class ParkRopeAxes(ctypes.Structure):
+    _fields_ = [("extent", ctypes.c_int * 3), ("pairs", ctypes.c_int * 3), ("half", ctypes.c_int),
+                ("table", ctypes.c_void_p)]
+
+
+class ParkAttnShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("Nq", ctypes.c_int64),
+                ("Nk", ctypes.c_int64), ("n_seq", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class ParkError(RuntimeError):
@@ -110,6 +129,22 @@ def load() -> ctypes.CDLL:
     lib.park_qrkc_metric_static.restype = i32
     lib.park_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.park_set_wait_limit_ns.restype = i32
+    op, axes, att, i64 = (ctypes.POINTER(ParkOperand), ctypes.POINTER(ParkRopeAxes), ctypes.POINTER(ParkAttnShape),
+                          ctypes.c_int64)
+    lib.park_rope_table_floats.argtypes = [axes]
+    lib.park_rope_table_floats.restype = sz
+    lib.park_rope_table.argtypes = [axes, ctypes.c_double, ctypes.POINTER(ctypes.c_double), vp]
+    lib.park_rope.argtypes = [op, op, i32, i64, i32, i32, axes, vp, i64, i32, vp, vp]
+    lib.park_qk_norm_rope.argtypes = [op, op, vp, vp, i32, f32, axes, vp, i64, op, op, i32, i64, i32, i32, vp, vp]
+    lib.park_qk_norm_rope_bwd_workspace.argtypes = [i32, i64, i32, ctypes.POINTER(sz)]
+    lib.park_qk_norm_rope_bwd.argtypes = [op, op, op, op, vp, vp, i32, f32, axes, vp, i64, op, op, vp, vp, i32, i64,
+                                          i32, i32, vp, sz, vp, vp]
+    lib.park_attention_workspace.argtypes = [att, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.park_attention.argtypes = [att, op, op, op, op, vp, vp, sz, vp, vp]
+    lib.park_attention_bwd.argtypes = [att, op, op, op, op, op, vp, op, op, op, vp, sz, vp, vp]
+    for f in ("park_rope_table", "park_rope", "park_qk_norm_rope", "park_qk_norm_rope_bwd_workspace",
+              "park_qk_norm_rope_bwd", "park_attention_workspace", "park_attention", "park_attention_bwd"):
+        getattr(lib, f).restype = i32
     _lib = lib
     return lib
 

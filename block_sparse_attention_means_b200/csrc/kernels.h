@@ -196,4 +196,24 @@ int launch_sparse_attn_simt(const void* Q, const void* K, const void* V, int dty
                             const int32_t* kept_ptr, const int32_t* kept_idx, const float* bweight, void* O,
                             cudaStream_t st);
 
+// ---- k_rope.cu
+int launch_rope_table(const park_rope_axes* r, double theta, const double* scale, cudaStream_t st);
+// q (and k, or null) -> yq, yk: the rotation alone (norm false) or norm and rotation
+int launch_rope(const park_operand* q, const park_operand* k, const park_operand* yq, const park_operand* yk,
+                const void* wq, const void* wk, int wdtype, float eps, bool norm, const park_rope_axes* rope,
+                const int32_t* pos, long long pos_sb, bool inverse, int B, long long N, int D, int dtype,
+                int32_t* status, int num_sms, cudaStream_t st);
+int norm_rope_bwd_blocks(long long tokens);  // rows of `part`: float [blocks][2][D]
+int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const park_operand* q,
+                         const park_operand* k, const park_operand* dq, const park_operand* dk, const void* wq,
+                         const void* wk, int wdtype, float eps, const park_rope_axes* rope, const int32_t* pos,
+                         long long pos_sb, float* dwq, float* dwk, int B, long long N, int D, int dtype, float* part,
+                         int32_t* status, int num_sms, cudaStream_t st);
+
+// ---- k_dense.cu: dense attention (bounds and operands as in dense.cuh)
+struct DenseArgs;
+int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st);
+int launch_dense_fwd_simt(const DenseArgs& a, int dtype, cudaStream_t st);
+int launch_dense_bwd_simt(const DenseArgs& a, int dtype, const float* delta, cudaStream_t st);
+
 }  // namespace park

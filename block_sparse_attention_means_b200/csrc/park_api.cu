@@ -631,6 +631,7 @@ const char* park_status_string(int code) {
         case PARK_ERR_CUDA: return "CUDA launch failed";
         case PARK_ERR_RANGE: return "input outside the range precondition (0 or 2^-40 <= |x| < 2^40, finite)";
         case PARK_ERR_TIMEOUT: return "a bounded device wait ran out";
+        case PARK_ERR_INDEX: return "a position or a sequence bound is out of range";
         default: return "unknown status";
     }
 }
@@ -672,7 +673,7 @@ int park_profile_collect(park_kernel_time* out, int cap, int* n) {
     return rc;
 }
 
-int park_version(void) { return 200; }
+int park_version(void) { return 300; }
 
 int park_set_wait_limit_ns(uint64_t ns) {
     g_wait_ns.store(ns ? ns : kDefaultWaitNs, std::memory_order_relaxed);

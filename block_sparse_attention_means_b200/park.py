@@ -174,8 +174,13 @@ def sparse_attn(Q, K, V, shape: Shape, NQ: int, NK: int, r: Retrieval, O: torch.
 
 
 def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torch.Tensor | None = None,
-          out: Retrieval | None = None, ws: torch.Tensor | None = None, stream=None):
-    """Retrieval + block-sparse attention; returns (O, Retrieval)."""
+          out: Retrieval | None = None, ws: torch.Tensor | None = None, stream=None, pre=None):
+    """Retrieval + block-sparse attention; returns (O, Retrieval).  pre (an ops.NormRope):
+    Q and K are the raw projections, in any layout that the operators take, and are
+    normed and rotated first; conditions that pre meets go to the result's status word
+    of ops.status_word(device)."""
+    if pre is not None:
+        Q, K = pre(Q, K, stream=stream)
     _check_inputs(shape, Q, K, V)
     O = O if O is not None else torch.empty_like(Q)
     out = out or alloc_retrieval(shape, NQ, NK, Q.device)

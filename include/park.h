@@ -69,6 +69,7 @@ extern "C" {
 #define PARK_ERR_CUDA 4        /* a kernel launch or memset failed            */
 #define PARK_ERR_RANGE 5       /* device: input outside the range precondition */
 #define PARK_ERR_TIMEOUT 6     /* device: a bounded wait ran out              */
+#define PARK_ERR_INDEX 7       /* device: a position or sequence bound out of range */
 
 /* ---- element types ----------------------------------------------------- */
 #define PARK_BF16 0
@@ -242,6 +243,120 @@ int park_version(void);
  * limit (1 ns) makes the waits run out on purpose: that is how the timeout path
  * is tested.  Never needed in normal use. */
 int park_set_wait_limit_ns(uint64_t ns);
+
+/* ---- operators before and beside the layer ------------------------------
+ * Rotary positions over (time, height, width), the RMS norm of queries and keys
+ * for each head with the rotation in the same pass, and dense attention over
+ * whole prompts.  They take any 16-byte aligned layout of [B, H, N, D] (a fused
+ * projection's [B, N, 3, H, D] is read in place), D a multiple of 32 up to 128,
+ * and PARK_BF16 or PARK_F32.
+ *   - Range: any finite input (no 2^-40 .. 2^40 precondition); sums of squares
+ *     are held in float32, so a norm's rows need sum x^2 < 2^127.
+ *   - *status (device, int32[1], not NULL) is written only when a device-side
+ *     condition is met and never cleared by these calls: zero it once, read it
+ *     whenever convenient; calls may share it.
+ *   - Outputs may not overlap inputs or one another, except that park_rope,
+ *     park_qk_norm_rope and park_qk_norm_rope_bwd may write an output onto an input
+ *     of the same side (same pointer and strides). */
+
+/* One tensor [B, H, N, D]: element (b, h, n, d) at ptr + b*sb + h*sh + n*sn + d
+ * (strides in elements).  ptr 16-byte aligned; every stride of an axis longer
+ * than 1 a positive multiple of 16 bytes; the elements of an output distinct. */
+typedef struct {
+    void *ptr;
+    int H;
+    int64_t sb, sh, sn;
+} park_operand;
+
+/* Rotary axes.  The table holds, for each axis a (time, height, width) with
+ * extent E_a and n_a = pairs[a] rotated pairs, (cos, sin) of
+ * (scale_a pos) theta^(-j / n_a) as float2 [E_a][n_a], the axes one after the
+ * other: park_rope_table_floats() floats, 8-byte aligned.  Pair j of the head is
+ * (2j, 2j+1), with half != 0 (j, j + D/2); the axes own consecutive pairs, the
+ * last D/2 - n_0 - n_1 - n_2 pairs are not rotated. */
+typedef struct {
+    int extent[3];
+    int pairs[3];
+    int half;
+    float *table;
+} park_rope_axes;
+
+/* Host only: floats of the table, 0 for bad axes. */
+size_t park_rope_table_floats(const park_rope_axes *rope);
+
+/* Fills rope->table (angles and their cos/sin in float64, rounded once). */
+int park_rope_table(const park_rope_axes *rope, double theta, const double scale[3], void *stream);
+
+/* y = x rotated by each token's position; inverse != 0 rotates back, which is
+ * also the gradient (dx from dy).  positions: device int32 [N][3] (t, y, w) for
+ * each token, batch b's at positions + b*pos_sb (0 = shared by the batch); a token
+ * with a negative coordinate is text and is not rotated; a coordinate at or above
+ * its extent sets *status to PARK_ERR_INDEX and leaves the token unrotated.
+ * positions NULL: the grid order of park_shape, token n = (t Hg + y) W + w, tokens
+ * behind the grid (text) not rotated. */
+int park_rope(const park_operand *x, const park_operand *y, int B, int64_t N, int D, int dtype,
+              const park_rope_axes *rope, const int32_t *positions, int64_t pos_sb, int inverse, int32_t *status,
+              void *stream);
+
+/* For each head row of Q and K: y = R(w x / sqrt(mean x^2 + eps)), computed in
+ * float32 and rounded once.  wq, wk: [D] in wdtype (PARK_BF16 or PARK_F32), NULL =
+ * all ones.  rope NULL: no rotation (positions must then be NULL).  eps > 0. */
+int park_qk_norm_rope(const park_operand *q, const park_operand *k, const void *wq, const void *wk, int wdtype,
+                      float eps, const park_rope_axes *rope, const int32_t *positions, int64_t pos_sb,
+                      const park_operand *q_out, const park_operand *k_out, int B, int64_t N, int D, int dtype,
+                      int32_t *status, void *stream);
+
+/* Gradients of park_qk_norm_rope from the gradients of its outputs and its own
+ * inputs: dq, dk in the inputs' type; dwq, dwk float32 [D] (NULL: not wanted).  The
+ * sums over rows are taken in a fixed order: the same call gives the same bits. */
+int park_qk_norm_rope_bwd_workspace(int B, int64_t N, int D, size_t *bytes);
+int park_qk_norm_rope_bwd(const park_operand *dq_out, const park_operand *dk_out, const park_operand *q,
+                          const park_operand *k, const void *wq, const void *wk, int wdtype, float eps,
+                          const park_rope_axes *rope, const int32_t *positions, int64_t pos_sb,
+                          const park_operand *dq, const park_operand *dk, float *dwq, float *dwk, int B, int64_t N,
+                          int D, int dtype, void *ws, size_t ws_bytes, int32_t *status, void *stream);
+
+/* Dense attention, softmax(scale q k^T) v over whole sequences.
+ *   n_seq == 0: each of the B batch entries is one sequence of Nq query rows and
+ *               Nk key rows; cu_q, cu_k unused.
+ *   n_seq  > 0: packed (B == 1): sequence s has query rows cu_q[s] .. cu_q[s+1]-1 of
+ *               Nq and key rows cu_k[s] .. cu_k[s+1]-1 of Nk; cu_q, cu_k are device
+ *               int32 [n_seq + 1], rising.  Empty sequences are allowed, rows outside
+ *               every sequence are neither read nor written.  A sequence whose bounds
+ *               are not 0 <= cu[s] <= cu[s+1] <= N sets *status to PARK_ERR_INDEX and is
+ *               skipped.
+ *   causal:     row i of a sequence sees keys j <= i + (n_k - n_q): the last row sees
+ *               every key, rows without a key give 0 (and lse = -inf).
+ *   heads:      Q and O have Hq heads, K and V Hk; Hk divides Hq and query head h reads
+ *               key head h / (Hq / Hk).
+ * What a mask hides does not reach a row: keys and values behind it may hold
+ * infinities or NaN.  Sums are float32; bf16 probabilities round once before their
+ * product with v (and, in the gradients, the probabilities and the gradients of the
+ * scores before theirs).  Every sum runs in a fixed order. */
+typedef struct {
+    int B, D, dtype;
+    int64_t Nq, Nk;
+    int n_seq;
+    const int32_t *cu_q, *cu_k;
+    int causal;
+    float scale;
+} park_attn_shape;
+
+/* Device workspace of park_attention (backward == 0) or park_attention_bwd
+ * (backward != 0); 0 bytes is possible.  Host only. */
+int park_attention_workspace(const park_attn_shape *shape, int Hq, int Hk, int backward, size_t *bytes);
+
+/* lse: float32 [B, Hq, Nq], log sum exp of each row's scaled scores, or NULL. */
+int park_attention(const park_attn_shape *shape, const park_operand *q, const park_operand *k, const park_operand *v,
+                   const park_operand *o, float *lse, void *ws, size_t ws_bytes, int32_t *status, void *stream);
+
+/* Gradients from o and lse of park_attention and the gradient of o.  dk, dv are sums
+ * over the query heads that share a key head.  Rows outside every sequence are left
+ * as they were. */
+int park_attention_bwd(const park_attn_shape *shape, const park_operand *d_o, const park_operand *q,
+                       const park_operand *k, const park_operand *v, const park_operand *o, const float *lse,
+                       const park_operand *dq, const park_operand *dk, const park_operand *dv, void *ws,
+                       size_t ws_bytes, int32_t *status, void *stream);
 
 /* ---- per-kernel timing for measurement tools --------------------------- */
 typedef struct {
