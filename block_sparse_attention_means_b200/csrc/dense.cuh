@@ -20,6 +20,15 @@ struct DenseArgs {
     int32_t* status;
 };
 
+// How the forward pass on the tensor cores cuts its work: row tiles of a key head, parts that the
+// keys are split into (1: none) and the key tiles of a part; workspace for the parts.
+struct DenseSplit {
+    long long tiles;
+    int n, chunk;
+    size_t lse_off, bytes;
+};
+constexpr int kDenseSMs = 148;  // SMs of a B200
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

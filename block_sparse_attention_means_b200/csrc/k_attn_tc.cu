@@ -562,30 +562,45 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::mutex g_encode_mu;
 }  // namespace
 
-// 2-D bf16 tensor [rows][cols] (row-major), boxes of 64 columns x box_rows,
-// 128-byte swizzle.  The driver entry point is looked up once.
-int make_tma_map_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows) {
-    {
-        std::lock_guard<std::mutex> lk(g_encode_mu);
-        if (!g_encode) {
-            void* fn = nullptr;
-            cudaDriverEntryPointQueryResult q;
-            if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
-                q != cudaDriverEntryPointSuccess || !fn) {
-                cudaGetLastError();
-                return PARK_ERR_CUDA;
-            }
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+// bf16 tensor maps with boxes 64 columns wide and 128-byte swizzle: 2-D [rows][cols] (row-major), or 4-D with
+// byte strides of the three outer axes.  The driver entry point is looked up once.
+static int tma_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+    std::lock_guard<std::mutex> lk(g_encode_mu);
+    if (!g_encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn) {
+            cudaGetLastError();
+            return PARK_ERR_CUDA;
         }
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    cuuint32_t box[2] = {64, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    *out = g_encode;
+    return PARK_OK;
+}
+
+static int encode_bf16(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    PARK_CHECK(tma_encoder(&encode));
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PARK_OK : PARK_ERR_CUDA;
+}
+
+int make_tma_map_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    return encode_bf16(map, ptr, 2, dims, strides, box);
+}
+
+int make_tma_map_4d(CUtensorMap* map, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* box) {
+    return encode_bf16(map, ptr, 4, dims, strides, box);
 }
 
 size_t attn_tc_smem_bytes() { return (size_t)(2 + 2 * TC_KST + 2 * TC_VST) * TC_BLK + 1024; }  // Q, K and V rings

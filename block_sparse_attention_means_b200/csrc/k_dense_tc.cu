@@ -1,0 +1,546 @@
+// Dense attention, forward, bf16 on the 5th-generation tensor cores.
+//
+//   o_i = sum_j p_ij v_j / l_i,  p_ij = 2^(s_ij log2(e) scale - m_i),  one pass over the keys
+//
+// A CTA owns 256 query rows as two tiles of 128 ("stages") over one key head.  With
+// grouped heads the rows of a sequence are counted token by token, the group's heads
+// side by side (row r = token r / G, head r % G), so a single token fills G rows and
+// its keys are read once for the whole group.  K and V arrive by TMA in tiles of 128
+// keys (one ring for both); the head dimension is padded to 64 or 128 by the copy's
+// zero fill.  Tensor memory: S_0 | S_1 (128 columns each) | O_0 | O_1.  Per key tile
+// and stage: S = Q K^T; the stage's four warps, one thread a row, turn S into P (bf16,
+// over S's own columns, the A operand of the next product); O += P V.  The two stages
+// alternate, so the tensor cores work on one while the other is in its Softmax:
+//   S0(j+1) follows PV0(j), S1(j+1) follows PV1(j), MMAs of one thread run in issue order,
+// which also means that s_full(j+1) implies that PV(j) is done: a stage may then rescale
+// its O.  It does so only when its running maximum grows by more than 2^8 (P stays
+// below 2^8, exact in the end since O and l carry the same reference).
+//
+// P is rounded to bf16 (the MMA's operand type), l sums the unrounded values.
+//
+// Warps 0-7: Softmax (stage = warp / 4) and epilogue; 8: TMA; 9: MMA; 10: forwards the V
+// tiles to the MMA warp and, in tiles that a mask cuts, replaces infinities and NaN by 0:
+// 0 x NaN is NaN, so a hidden row would reach all rows of its tile.  What the rows do see
+// of them is added in the epilogue.
+//
+// When the row tiles do not fill the GPU, the keys are split over CTAs; each writes its
+// part's normalised O in float32 and its log-sum-exp, and k_dense_combine joins them.
+//
+// Every wait is time-bounded (PARK_ERR_TIMEOUT); on a failed wait the roles leave their
+// loops, copies and MMAs in flight are waited for and TMEM is freed.
+#include "dense.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace park {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kTile = 128;             // keys of a tile, query rows of a stage
+constexpr uint32_t kPanel = 16384;     // 128 rows of 64 bf16
+constexpr float kRescale = 8.f;        // log2 units
+constexpr int kClean = 4;              // V tiles that the ring can hold at once, at most
+
+template <int NP>
+struct FwdCfg {  // NP: 64-column panels of the padded head dimension
+    static constexpr int ST = NP == 2 ? 5 : 8;  // ring stages (K and V tiles)
+    static constexpr uint32_t tile = NP * kPanel;
+    static constexpr size_t smem = (size_t)(2 + ST) * tile + 1024;
+};
+
+struct FwdSmem {
+    uint64_t q_full[2], kv_full[8], kv_empty[8], v_clean[kClean], s_full[2], p_full[2][2], o_full[2], final_bar;
+    uint32_t tmem_base;
+    int abort, poison;
+    SeqTile seq;
+};
+
+__device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int n, int h, int b) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
+        : "memory");
+}
+// a 16-byte piece with an infinity or NaN among its bf16
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
+struct Piece {
+    int r0, rows, nt[2], j_lo, jmax;
+};
+__device__ __forceinline__ Piece fwd_piece(const SeqTile& t, int G, int causal, int n_split, int sp, int chunk) {
+    Piece p;
+    p.r0 = t.tile * 2 * kTile;
+    p.rows = t.live ? min(2 * kTile, t.nq * G - p.r0) : 0;
+    p.j_lo = n_split > 1 ? sp * chunk : 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int last = min(p.rows, (s + 1) * kTile) - 1;  // last row of the stage
+        int n = 0;
+        if (last >= s * kTile) {
+            const int kend = dense_last_key((p.r0 + last) / G, t.nq, t.nk, causal) + 1;
+            n = kend > 0 ? (kend + kTile - 1) / kTile : 0;
+            n = max(0, (n_split > 1 ? min(n, p.j_lo + chunk) : n) - p.j_lo);
+        }
+        p.nt[s] = n;
+    }
+    p.jmax = max(p.nt[0], p.nt[1]);
+    return p;
+}
+
+template <int NP>
+__global__ void __launch_bounds__(384, 1)
+    k_dense_fwd_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
+                   int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse, uint64_t wait_ns) {
+    using C = FwdCfg<NP>;
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    __shared__ FwdSmem sh;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+    uint8_t* Qs = base;                 // two tiles
+    uint8_t* Ks = base + 2 * C::tile;   // ring
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort = &sh.abort;
+    if (warp == 0) {
+        const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, 2 * kTile, false, a.Hq / a.Hk);
+        if (lane == 0) {
+            sh.seq = t;
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(&sh.q_full[s], 128);
+                mbar_init(&sh.s_full[s], 1);
+                mbar_init(&sh.p_full[s][0], 128);
+                mbar_init(&sh.p_full[s][1], 128);
+                mbar_init(&sh.o_full[s], 1);
+            }
+            for (int s = 0; s < C::ST; ++s) {
+                mbar_init(&sh.kv_full[s], 1);
+                mbar_init(&sh.kv_empty[s], 1);
+            }
+            for (int s = 0; s < kClean; ++s) mbar_init(&sh.v_clean[s], 1);
+            mbar_init(&sh.final_bar, 1);
+            sh.abort = 0;
+            sh.poison = 0;
+            mbar_fence_init();
+        }
+    } else if (warp == 9) {
+        tmem_alloc(&sh.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    const SeqTile t = sh.seq;
+    const int G = a.Hq / a.Hk, hk = blockIdx.y;
+    const int b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split;
+    const Piece pc = fwd_piece(t, G, a.causal, n_split, sp, chunk);
+    // first key tile (counted within the piece) that some row does not see whole
+    const int cut = (dense_last_key(pc.r0 / G, t.nq, t.nk, a.causal) + 1) / kTile - pc.j_lo;
+
+    if (warp >= 8) {
+        reg_dec<56>();
+        if (warp == 8 && lane == 0) {
+            // ---------------------------------------------------------------- TMA
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            int issued = 0;
+            bool ok = true;
+            for (int i = 0; i < 2 * pc.jmax && ok; ++i) {  // K_0 V_0 K_1 V_1 ...
+                const int st = i % C::ST, round = i / C::ST;
+                if (round > 0 && !mbar_wait(&sh.kv_empty[st], (round - 1) & 1, abort, wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sh.kv_full[st], C::tile);
+                const int n = t.k0 + (pc.j_lo + (i >> 1)) * kTile;
+                for (int p = 0; p < NP; ++p)
+                    tma_load_4d(Ks + st * C::tile + p * kPanel, i & 1 ? &tmV : &tmK, &sh.kv_full[st], 64 * p, n, hk, b);
+                ++issued;
+            }
+            int dummy = 0;  // copies in flight land before the CTA may exit
+            for (int i = max(0, issued - C::ST); i < issued; ++i)
+                mbar_wait(&sh.kv_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
+        } else if (warp == 9 && lane == 0) {
+            // ---------------------------------------------------------------- MMA
+            const uint32_t idS = idesc_bf16(128, 128, 0, 0), idO = idesc_bf16(128, 64 * NP, 0, 1);
+            auto issue_S = [&](int s, int j) -> bool {
+                const int i = 2 * j, st = i % C::ST;
+                if (!mbar_wait(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
+                tc_fence_after();
+                const uint32_t qa = smem_u32(Qs) + s * C::tile, ka = smem_u32(Ks) + st * C::tile;
+#pragma unroll
+                for (int kk = 0; kk < 4 * NP; ++kk) {
+                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
+                    umma_bf16(tmem + 128 * s, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idS,
+                              kk > 0);
+                }
+                umma_commit(&sh.s_full[s]);
+                // the last stage that uses K_j frees it
+                if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.kv_empty[st]);
+                return true;
+            };
+            bool ok = true;
+            for (int s = 0; s < 2 && ok; ++s)
+                if (pc.nt[s] > 0) {
+                    ok = mbar_wait(&sh.q_full[s], 0, abort, wait_ns);
+                    if (ok) {
+                        tc_fence_after();
+                        ok = issue_S(s, 0);
+                    }
+                }
+            for (int j = 0; j < pc.jmax && ok; ++j) {
+                const int i = 2 * j + 1, st = i % C::ST;
+                const uint32_t va = smem_u32(Ks) + st * C::tile;
+                if (!mbar_wait(&sh.v_clean[j % kClean], (j / kClean) & 1, abort, wait_ns)) break;
+                for (int s = 0; s < 2 && ok; ++s) {
+                    if (j >= pc.nt[s]) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!mbar_wait(&sh.p_full[s][h], j & 1, abort, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            umma_bf16_ts(tmem + 256 + 64 * NP * s, tmem + 128 * s + 8 * kk,
+                                         sdesc_sw128(va + kk * 2048, kPanel, 1024), idO, j > 0 || kk > 0);
+                    }
+                    if (!ok) break;
+                    if (j + 1 == pc.nt[s]) umma_commit(&sh.o_full[s]);
+                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.kv_empty[st]);
+                    if (j + 1 < pc.nt[s]) ok = issue_S(s, j + 1);
+                }
+            }
+            umma_commit(&sh.final_bar);  // every MMA is done before TMEM is released
+            int dummy = 0;
+            mbar_wait(&sh.final_bar, 0, &dummy, 100000000ull);
+        } else if (warp == 10) {
+            // ---------------------------------------------------------------- V tiles: forward, clean where cut
+            for (int j = 0; j < pc.jmax; ++j) {
+                const int i = 2 * j + 1, st = i % C::ST;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns))) break;
+                if (j >= cut) {
+                    const int n0 = (pc.j_lo + j) * kTile;
+                    uint4* v = reinterpret_cast<uint4*>(Ks + st * C::tile);
+                    for (int e = lane; e < (int)(C::tile / 16); e += 32) {
+                        uint4 w = v[e];
+                        if (nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w)) {
+                            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t f = nonfinite2(u[x]);
+                                u[x] &= ~(((f >> 15) & 0x00010001u) * 0xFFFFu);
+                            }
+                            v[e] = w;
+                            if (n0 + (e >> 3) % kTile < t.nk) sh.poison = 1;  // (128 rows of 8 pieces to a panel)
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __threadfence_block();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.v_clean[j % kClean]);
+            }
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------------------- Softmax
+        reg_inc<216>();
+        const int s = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
+        const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint32_t scol = trow + 128 * s, ocol = trow + 256 + 64 * NP * s;
+        const int nt = pc.nt[s];
+        const int r = pc.r0 + kTile * s + row;
+        const int tok = r / G, head = hk * G + (r - tok * G);
+        const bool live = kTile * s + row < pc.rows;
+        if (nt > 0) {
+            // the warp's 32 query rows, 8 NP pieces of 16 bytes each, into the swizzled tile
+            constexpr int PR = 8 * NP;
+            uint8_t* qt = Qs + s * C::tile;
+            const int chunks = a.D / 8;
+#pragma unroll 4
+            for (int e = lane; e < 32 * PR; e += 32) {
+                const int rr = 32 * quad + e / PR, c = e % PR;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (kTile * s + rr < pc.rows && c < chunks) {
+                    const int rg = pc.r0 + kTile * s + rr, tk = rg / G, hh = hk * G + (rg - tk * G);
+                    v = __ldg(reinterpret_cast<const uint4*>(a.q.p + (b * a.q.sb + hh * a.q.sh + (t.q0 + tk) * a.q.sn) * 2) + c);
+                }
+                *reinterpret_cast<uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.q_full[s]);
+        }
+        const float sl2 = a.scale * kLog2e, NI = __int_as_float(0xff800000);
+        const float2 sl22 = make_float2(sl2, sl2);
+        const int seen = live ? dense_last_key(tok, t.nq, t.nk, a.causal) : -1;  // last visible key
+        float m = NI;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[s], j & 1, abort, wait_ns))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, x[c]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_dep(x[c]);
+            if (j >= cut) {
+                const int lim = seen - (pc.j_lo + j) * kTile;  // columns 0 .. lim are visible
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > lim) x[c][e] = 0xff800000u;
+            }
+            float tm[4] = {NI, NI, NI, NI};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) tm[(e >> 1) & 3] = max3(tm[(e >> 1) & 3], f_of(x[c][e]), f_of(x[c][e + 1]));
+            const float tmax = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sl2;
+            if (j == 0) {
+                m = tmax;
+            } else if (__any_sync(0xffffffffu, tmax > m + kRescale)) {
+                // decided per warp; rows that keep their reference get a factor of 1
+                const float mn = tmax > m + kRescale ? tmax : m;
+                const float f = mn == m ? 1.f : ex2(m - mn);
+#pragma unroll
+                for (int c = 0; c < 2 * NP; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(ocol + 32 * c, o);
+                    tmem_ld_wait();
+                    tmem_ld_dep(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * f);
+                    tmem_st32(ocol + 32 * c, o);
+                }
+                l2.x *= f;
+                l2.y *= f;
+                m = mn;
+            }
+            const float mr = m == NI ? 0.f : m;  // a row that has seen no key yet: P = 0
+            const float2 nm = make_float2(-mr, -mr);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 d = __ffma2_rn(make_float2(f_of(x[c][2 * e]), f_of(x[c][2 * e + 1])), sl22, nm);
+                    const float p0 = ex2(d.x), p1 = ex2(d.y);
+                    l2 = __fadd2_rn(l2, make_float2(p0, p1));
+                    pk[e] = bf2(p0, p1);
+                }
+                tmem_st16(scol + 16 * c, pk);
+                if (c & 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&sh.p_full[s][c >> 1]);
+                }
+            }
+        }
+        // ---------------------------------------------------------------- epilogue
+        float l = l2.x + l2.y;
+        if (nt > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.o_full[s], 0, abort, wait_ns));
+        if (ok) {
+            tc_fence_after();
+            const bool none = m == NI && l == 0.f;  // no visible key (or every score -inf)
+            const float inv = none ? 0.f : 1.f / l;
+            const size_t row_id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
+            const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
+            const bool split = n_split > 1;
+            if (live) {
+                const float lse = none ? NI : (m + log2f(l));
+                if (split)
+                    part_lse[sp * rows_all + row_id] = lse;
+                else if (a.lse)
+                    a.lse[row_id] = lse * kLn2;
+            }
+            uint8_t* orow = a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2;
+            float* prow = part_o + (sp * rows_all + row_id) * a.D;
+            if (!(split && nt == 0)) {  // (a part without keys is only its lse)
+#pragma unroll
+                for (int c = 0; c < 2 * NP; ++c) {
+                    if (32 * c >= a.D) break;
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (nt > 0) {
+                        tmem_ld32(ocol + 32 * c, o);
+                        tmem_ld_wait();
+                        tmem_ld_dep(o);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = nt > 0 && !none ? __float_as_uint(f_of(o[e]) * inv) : 0u;
+                    if (sh.poison && live) {  // infinities and NaN that the row does see in the cut tiles
+                        const int k1 = min(seen + 1, (pc.j_lo + nt) * kTile);
+                        for (int key = max(0, pc.j_lo + cut) * kTile; key < k1; ++key) {
+                            const uint16_t* vr = reinterpret_cast<const uint16_t*>(
+                                                     a.v.p + (b * a.v.sb + hk * a.v.sh + (t.k0 + (long long)key) * a.v.sn) * 2) + 32 * c;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if ((vr[e] & 0x7F80u) == 0x7F80u)
+                                    o[e] = __float_as_uint(f_of(o[e]) + f_of((uint32_t)vr[e] << 16));
+                        }
+                    }
+                    if (live && split) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(prow + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(orow + 2 * (32 * c + e)) =
+                                make_uint4(bf2(f_of(o[e]), f_of(o[e + 1])), bf2(f_of(o[e + 2]), f_of(o[e + 3])),
+                                           bf2(f_of(o[e + 4]), f_of(o[e + 5])), bf2(f_of(o[e + 6]), f_of(o[e + 7])));
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && sh.abort) set_status(a.status, PARK_ERR_TIMEOUT);
+}
+
+// Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum; one warp a row.
+__global__ void __launch_bounds__(256)
+    k_dense_combine(DenseArgs a, int n_split, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+    __shared__ SeqTile sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
+    if (warp == 0) {
+        const SeqTile t = dense_resolve(a, blockIdx.x, 2 * kTile, false, G);
+        if (lane == 0) sh = t;
+    }
+    __syncthreads();
+    const SeqTile t = sh;
+    if (!t.live) return;
+    const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
+    const int r1 = min(t.nq * G, (t.tile + 1) * 2 * kTile);
+    for (int r = t.tile * 2 * kTile + warp; r < r1; r += 8) {
+        const int tok = r / G, head = hk * G + (r - tok * G);
+        const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
+        float M = __int_as_float(0xff800000);
+        for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
+        M = warp_max(M);
+        const bool none = M == __int_as_float(0xff800000);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int s = 0; s < n_split; ++s) {
+            const float ls = part_lse[s * rows_all + id];
+            if (ls == __int_as_float(0xff800000)) continue;  // (its part of o may not be written)
+            const float w = ex2(ls - M);
+            sum += w;
+            if (4 * lane < a.D) {
+                const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
+                acc.x = fmaf(w, o.x, acc.x);
+                acc.y = fmaf(w, o.y, acc.y);
+                acc.z = fmaf(w, o.z, acc.z);
+                acc.w = fmaf(w, o.w, acc.w);
+            }
+        }
+        const float inv = none ? 0.f : 1.f / sum;
+        if (4 * lane < a.D)
+            *reinterpret_cast<uint2*>(a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2 + 8 * lane) =
+                make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+        if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
+    }
+}
+
+// 4-D map [B][H][N][D], boxes of 64 x box_rows, 128-byte swizzle; what lies past D or N reads as 0.
+int map_4d(CUtensorMap* m, const Op4& op, int B, int H, long long N, int D, int box_rows) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
+    // strides of axes of length 1 are never used: any valid value does
+    const cuuint64_t st[3] = {(cuuint64_t)(N > 1 ? op.sn * 2 : 256), (cuuint64_t)(H > 1 ? op.sh * 2 : 256),
+                              (cuuint64_t)(B > 1 ? op.sb * 2 : 256)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    return make_tma_map_4d(m, op.p, dims, st, box);
+}
+
+template <int NP>
+int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, const DenseSplit& sp, float* part_o,
+           float* part_lse, cudaStream_t st) {
+    cudaFuncSetAttribute(k_dense_fwd_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdCfg<NP>::smem);
+    const dim3 grid((unsigned)sp.tiles, a.Hk, a.B * sp.n);
+    ::park::prof_begin(st);
+    k_dense_fwd_tc<NP><<<grid, 384, FwdCfg<NP>::smem, st>>>(mK, mV, a, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
+    PARK_TRY_LAUNCH("k_dense_fwd_tc", st);
+    return PARK_OK;
+}
+
+}  // namespace
+
+DenseSplit dense_split(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
+    DenseSplit s;
+    s.tiles = dense_tiles(Nq * (Hq / Hk), n_seq, 2 * kTile);
+    s.n = 1;
+    s.chunk = 0;
+    const long long kt = (Nk + kTile - 1) / kTile + (n_seq > 0 ? n_seq : 0), ctas = s.tiles * Hk * B;
+    if (ctas * 2 <= kDenseSMs && kt > 8) {
+        // Parts of equal length whatever the sequence (a packed batch holds at most kt key tiles in
+        // all, one of a batch's entries as many), about two waves of them, at least 4 tiles each.
+        const long long work = (n_seq > 0 ? kt : kt * B) * Hk * (n_seq > 0 ? 1 : s.tiles);
+        long long chunk = (work + 2 * kDenseSMs - 1) / (2 * kDenseSMs);
+        if (chunk < 4) chunk = 4;
+        s.n = (int)((kt + chunk - 1) / chunk);
+        s.chunk = (int)chunk;
+        if (s.n <= 1) s.n = 1;
+    }
+    const size_t rows = (size_t)B * Hq * Nq;
+    s.lse_off = s.n > 1 ? align_up((size_t)s.n * rows * D * 4, 256) : 0;
+    s.bytes = s.n > 1 ? s.lse_off + align_up((size_t)s.n * rows * 4, 256) : 0;
+    return s;
+}
+
+int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
+    const DenseSplit sp = dense_split(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
+    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    CUtensorMap mK, mV;
+    // without keys nothing is loaded; the maps still have to be valid
+    PARK_CHECK(map_4d(&mK, a.Nk ? a.k : a.q, a.Nk ? a.B : 1, a.Nk ? a.Hk : 1, a.Nk ? a.Nk : 1, a.D, kTile));
+    PARK_CHECK(map_4d(&mV, a.Nk ? a.v : a.q, a.Nk ? a.B : 1, a.Nk ? a.Hk : 1, a.Nk ? a.Nk : 1, a.D, kTile));
+    float* part_o = static_cast<float*>(ws);
+    float* part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sp.lse_off);
+    PARK_CHECK(a.D <= 64 ? fwd_tc<1>(a, mK, mV, sp, part_o, part_lse, st)
+                         : fwd_tc<2>(a, mK, mV, sp, part_o, part_lse, st));
+    if (sp.n == 1) return PARK_OK;
+    ::park::prof_begin(st);
+    k_dense_combine<<<dim3((unsigned)sp.tiles, a.Hk, a.B), 256, 0, st>>>(a, sp.n, part_o, part_lse);
+    PARK_TRY_LAUNCH("k_dense_combine", st);
+    return PARK_OK;
+}
+
+}  // namespace park

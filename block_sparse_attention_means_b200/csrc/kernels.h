@@ -215,5 +215,11 @@ struct DenseArgs;
 int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st);
 int launch_dense_fwd_simt(const DenseArgs& a, int dtype, cudaStream_t st);
 int launch_dense_bwd_simt(const DenseArgs& a, int dtype, const float* delta, cudaStream_t st);
+// ---- k_dense_tc.cu: bf16 on tcgen05
+struct DenseSplit;
+DenseSplit dense_split(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D);
+int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st);
+int make_tma_map_4d(CUtensorMap* map, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* box);
 
 }  // namespace park

@@ -88,7 +88,7 @@ int sm_count() {
 int check_attn(const park_attn_shape* s, int Hq, int Hk) {
     if (!s || s->B < 1 || s->Nq < 0 || s->Nk < 0 || s->n_seq < 0 || Hq < 1 || Hk < 1) return PARK_ERR_INVALID_ARG;
     PARK_CHECK(check_head_dim(s->D, s->dtype));
-    if (Hq % Hk != 0 || !std::isfinite(s->scale)) return PARK_ERR_INVALID_ARG;
+    if (Hq % Hk != 0 || !std::isfinite(s->scale) || !(s->scale > 0.f)) return PARK_ERR_INVALID_ARG;
     if (s->n_seq > 0 && (s->B != 1 || !s->cu_q || !s->cu_k)) return PARK_ERR_INVALID_ARG;
     if (Hq > 65535 || s->B > 65535 || s->n_seq > (1 << 24)) return PARK_ERR_UNSUPPORTED;
     // rows of a key head's group, tiles and coordinates are int32
@@ -130,8 +130,10 @@ DenseArgs dense_args(const park_attn_shape* s, const park_operand* q, const park
 size_t delta_bytes(const park_attn_shape* s, int Hq) { return align_up((size_t)s->B * Hq * (size_t)s->Nq * 4, 256); }
 
 int attn_workspace(const park_attn_shape* s, int Hq, int Hk, int backward, size_t* bytes) {
-    (void)Hk;
-    *bytes = backward ? delta_bytes(s, Hq) : 0;
+    if (backward)
+        *bytes = delta_bytes(s, Hq);
+    else
+        *bytes = s->dtype == PARK_BF16 ? dense_split(s->B, Hq, Hk, s->Nq, s->Nk, s->n_seq, s->D).bytes : 0;
     return PARK_OK;
 }
 
@@ -242,7 +244,8 @@ int park_attention(const park_attn_shape* shape, const park_operand* q, const pa
     if (ws_bytes < need) return PARK_ERR_WORKSPACE;
     if (s->Nq == 0) return PARK_OK;
     const DenseArgs a = dense_args(s, q, k, v, o, lse, status);
-    return launch_dense_fwd_simt(a, s->dtype, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return s->dtype == PARK_BF16 ? launch_dense_fwd_tc(a, ws, st) : launch_dense_fwd_simt(a, s->dtype, st);
 }
 
 int park_attention_bwd(const park_attn_shape* shape, const park_operand* d_o, const park_operand* q,

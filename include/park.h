@@ -325,6 +325,7 @@ int park_qk_norm_rope_bwd(const park_operand *dq_out, const park_operand *dk_out
  *               every sequence are neither read nor written.  A sequence whose bounds
  *               are not 0 <= cu[s] <= cu[s+1] <= N sets *status to PARK_ERR_INDEX and is
  *               skipped.
+ *   scale:      positive and finite.
  *   causal:     row i of a sequence sees keys j <= i + (n_k - n_q): the last row sees
  *               every key, rows without a key give 0 (and lse = -inf).
  *   heads:      Q and O have Hq heads, K and V Hk; Hk divides Hq and query head h reads

@@ -136,6 +136,8 @@ def attention(s=None, q=None, k=None, v=None, o=None, status=FAKE):
     (dict(s=shape(dt=5)), _lib.PARK_ERR_INVALID_ARG),
     (dict(s=shape(scale=float("nan"))), _lib.PARK_ERR_INVALID_ARG),
     (dict(s=shape(scale=float("inf"))), _lib.PARK_ERR_INVALID_ARG),
+    (dict(s=shape(scale=0.0)), _lib.PARK_ERR_INVALID_ARG),
+    (dict(s=shape(scale=-0.1)), _lib.PARK_ERR_INVALID_ARG),
     (dict(s=shape(n_seq=-1)), _lib.PARK_ERR_INVALID_ARG),
     (dict(s=shape(n_seq=2, cu_q=FAKE, cu_k=FAKE)), _lib.PARK_ERR_INVALID_ARG),       # packed with B = 2
     (dict(s=shape(b=1, n_seq=2, cu_q=FAKE)), _lib.PARK_ERR_INVALID_ARG),
