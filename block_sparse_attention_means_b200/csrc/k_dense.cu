@@ -1,4 +1,4 @@
-// Dense attention in float32 arithmetic, forward and backward, and the row sums
+// Dense attention of float32 tensors, forward and backward, and the row sums
 // delta_i = sum_d do_id o_id that the backward pass of either type starts with.
 //
 // Forward: one pass over the keys with the running maximum m and sum l of the
@@ -37,13 +37,13 @@ __device__ __forceinline__ float4 load4<bf16_t>(const uint8_t* p, int i) {
 }
 
 // rows 0 .. n-1 of `src` (row stride in elements) into a [64][D + 4] tile, zeros below
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long long stride, int n) {
     constexpr int C = D / 4;
     for (int i = threadIdx.x; i < TB * C; i += 256) {
         const int r = i / C, c = i - r * C;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) v = load4<T>(src + r * stride * (long long)sizeof(T), c);
+        if (r < n) v = load4<float>(src + r * stride * 4, c);
         *reinterpret_cast<float4*>(dst + r * (D + 4) + 4 * c) = v;
     }
 }
@@ -101,16 +101,8 @@ __device__ __forceinline__ void accumulate(float (&acc)[4][D / 16], const float*
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store2(uint8_t* row, int col, float x, float y);
-template <>
-__device__ __forceinline__ void store2<float>(uint8_t* row, int col, float x, float y) {
+__device__ __forceinline__ void store2(uint8_t* row, int col, float x, float y) {
     *reinterpret_cast<float2*>(row + 4 * col) = make_float2(x, y);
-}
-template <>
-__device__ __forceinline__ void store2<bf16_t>(uint8_t* row, int col, float x, float y) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    *reinterpret_cast<uint32_t*>(row + 2 * col) = *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <typename T>
@@ -128,7 +120,7 @@ __device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, int x, bool
     return sh;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
@@ -141,7 +133,7 @@ __global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(TB, t.nq - i0);
-    load_tile<T, D>(Qs, row_ptr<T>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+    load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
     float acc[4][D / 16], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -154,8 +146,8 @@ __global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
     const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;  // keys that any row sees
     for (int j0 = 0; j0 < kend; j0 += TB) {
         __syncthreads();
-        load_tile<T, D>(Ks, row_ptr<T>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<T, D>(Vs, row_ptr<T>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
+        load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
+        load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
         __syncthreads();
         auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
         const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
@@ -200,10 +192,10 @@ __global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
         for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (r >= rows) continue;
         const float inv = m[i] == -INFINITY && !(sum != sum) ? 0.f : 1.f / sum;
-        uint8_t* row = row_ptr<T>(a.o, b, h, t.q0 + i0 + r);
+        uint8_t* row = row_ptr<float>(a.o, b, h, t.q0 + i0 + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            store2<T>(row, 2 * tx + 32 * c, inv == 0.f ? 0.f : acc[i][2 * c] * inv,
+            store2(row, 2 * tx + 32 * c, inv == 0.f ? 0.f : acc[i][2 * c] * inv,
                       inv == 0.f ? 0.f : acc[i][2 * c + 1] * inv);
         if (a.lse && tx == 0)
             a.lse[((size_t)b * a.Hq + h) * a.Nq + t.q0 + i0 + r] = (m[i] + log2f(sum)) * kLn2;
@@ -227,9 +219,7 @@ __global__ void __launch_bounds__(256) k_dense_delta(DenseArgs a, float* __restr
     if (lane == 0) delta[row] = s;
 }
 
-// ds tile (and the p tile when Pt is given) of a score tile: rows are queries in the
-// dq kernel (TR = false) and keys in the dk/dv kernel (TR = true).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float* __restrict__ delta) {
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
@@ -243,8 +233,8 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(TB, t.nq - i0);
-    load_tile<T, D>(Qs, row_ptr<T>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-    load_tile<T, D>(Gs, row_ptr<T>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
+    load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+    load_tile<D>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
     float acc[4][D / 16], lse2[4], del[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -259,8 +249,8 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
     const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;
     for (int j0 = 0; j0 < kend; j0 += TB) {
         __syncthreads();
-        load_tile<T, D>(Ks, row_ptr<T>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<T, D>(Vs, row_ptr<T>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
+        load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
+        load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
         __syncthreads();
         auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
         const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
@@ -285,14 +275,14 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= rows) continue;
-        uint8_t* row = row_ptr<T>(a.dq, b, h, t.q0 + i0 + r);
+        uint8_t* row = row_ptr<float>(a.dq, b, h, t.q0 + i0 + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            store2<T>(row, 2 * tx + 32 * c, acc[i][2 * c] * a.scale, acc[i][2 * c + 1] * a.scale);
+            store2(row, 2 * tx + 32 * c, acc[i][2 * c] * a.scale, acc[i][2 * c + 1] * a.scale);
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float* __restrict__ delta) {
     extern __shared__ __align__(16) float smem[];
     float* Ks = smem;
@@ -307,8 +297,8 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
     const int hk = blockIdx.y, b = blockIdx.z, G = a.Hq / a.Hk;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int keys = min(TB, t.nk - j0);
-    load_tile<T, D>(Ks, row_ptr<T>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
-    load_tile<T, D>(Vs, row_ptr<T>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
+    load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
+    load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
     float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -321,8 +311,8 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
         for (int i0 = first; i0 < t.nq; i0 += TB) {
             const int rows = min(TB, t.nq - i0);
             __syncthreads();
-            load_tile<T, D>(Qs, row_ptr<T>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-            load_tile<T, D>(Gs, row_ptr<T>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
+            load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+            load_tile<D>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
             __syncthreads();
             // r: key of the tile, c: query row of the tile
             auto see = [&](int r, int c) {
@@ -360,40 +350,40 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= keys) continue;
-        uint8_t* rk = row_ptr<T>(a.dk, b, hk, t.k0 + j0 + r);
-        uint8_t* rv = row_ptr<T>(a.dv, b, hk, t.k0 + j0 + r);
+        uint8_t* rk = row_ptr<float>(a.dk, b, hk, t.k0 + j0 + r);
+        uint8_t* rv = row_ptr<float>(a.dv, b, hk, t.k0 + j0 + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            store2<T>(rk, 2 * tx + 32 * c, dk[i][2 * c] * a.scale, dk[i][2 * c + 1] * a.scale);
-            store2<T>(rv, 2 * tx + 32 * c, dv[i][2 * c], dv[i][2 * c + 1]);
+            store2(rk, 2 * tx + 32 * c, dk[i][2 * c] * a.scale, dk[i][2 * c + 1] * a.scale);
+            store2(rv, 2 * tx + 32 * c, dv[i][2 * c], dv[i][2 * c + 1]);
         }
     }
 }
 
-template <typename T, int D>
+template <int D>
 int fwd_simt(const DenseArgs& a, cudaStream_t st) {
     const size_t sm = (size_t)(3 * TB * (D + 4) + TB * PP) * 4;
-    cudaFuncSetAttribute(k_dense_fwd_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    cudaFuncSetAttribute(k_dense_fwd_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     const dim3 grid((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B);
     ::park::prof_begin(st);
-    k_dense_fwd_simt<T, D><<<grid, 256, sm, st>>>(a);
+    k_dense_fwd_simt<D><<<grid, 256, sm, st>>>(a);
     PARK_TRY_LAUNCH("k_dense_fwd_simt", st);
     return PARK_OK;
 }
 
-template <typename T, int D>
+template <int D>
 int bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st) {
     const size_t sq = (size_t)(4 * TB * (D + 4) + TB * PP) * 4, sk = sq + (size_t)TB * PP * 4;
-    cudaFuncSetAttribute(k_dense_dq_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
-    cudaFuncSetAttribute(k_dense_dkv_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
+    cudaFuncSetAttribute(k_dense_dq_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
+    cudaFuncSetAttribute(k_dense_dkv_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
     if (a.Nq > 0) {
         ::park::prof_begin(st);
-        k_dense_dq_simt<T, D><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B), 256, sq, st>>>(a, delta);
+        k_dense_dq_simt<D><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B), 256, sq, st>>>(a, delta);
         PARK_TRY_LAUNCH("k_dense_dq_simt", st);
     }
     if (a.Nk == 0) return PARK_OK;
     ::park::prof_begin(st);
-    k_dense_dkv_simt<T, D><<<dim3((unsigned)dense_tiles(a.Nk, a.n_seq, TB), a.Hk, a.B), 256, sk, st>>>(a, delta);
+    k_dense_dkv_simt<D><<<dim3((unsigned)dense_tiles(a.Nk, a.n_seq, TB), a.Hk, a.B), 256, sk, st>>>(a, delta);
     PARK_TRY_LAUNCH("k_dense_dkv_simt", st);
     return PARK_OK;
 }
@@ -412,16 +402,14 @@ int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t
     return PARK_OK;
 }
 
-#define PARK_BY_D(T, F, ...)                                   \
-    (a.D == 32 ? F<T, 32>(__VA_ARGS__) : a.D == 64 ? F<T, 64>(__VA_ARGS__) \
-     : a.D == 96 ? F<T, 96>(__VA_ARGS__) : F<T, 128>(__VA_ARGS__))
+#define PARK_BY_D(F, ...)                                              \
+    (a.D == 32 ? F<32>(__VA_ARGS__) : a.D == 64 ? F<64>(__VA_ARGS__) \
+     : a.D == 96 ? F<96>(__VA_ARGS__) : F<128>(__VA_ARGS__))
 
-int launch_dense_fwd_simt(const DenseArgs& a, int dtype, cudaStream_t st) {
-    return dtype == PARK_BF16 ? PARK_BY_D(bf16_t, fwd_simt, a, st) : PARK_BY_D(float, fwd_simt, a, st);
-}
+int launch_dense_fwd_simt(const DenseArgs& a, cudaStream_t st) { return PARK_BY_D(fwd_simt, a, st); }
 
-int launch_dense_bwd_simt(const DenseArgs& a, int dtype, const float* delta, cudaStream_t st) {
-    return dtype == PARK_BF16 ? PARK_BY_D(bf16_t, bwd_simt, a, delta, st) : PARK_BY_D(float, bwd_simt, a, delta, st);
+int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st) {
+    return PARK_BY_D(bwd_simt, a, delta, st);
 }
 
 }  // namespace park

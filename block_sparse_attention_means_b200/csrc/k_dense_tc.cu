@@ -6,7 +6,8 @@
 // grouped heads the rows of a sequence are counted token by token, the group's heads
 // side by side (row r = token r / G, head r % G), so a single token fills G rows and
 // its keys are read once for the whole group.  K and V arrive by TMA in tiles of 128
-// keys (one ring for both); the head dimension is padded to 64 or 128 by the copy's
+// keys, each in its own ring (a wait for a phase is sound only for a role that has seen the
+// stage's phase before, and warp 10 sees V alone); the head dimension is padded to 64 or 128 by the copy's
 // zero fill.  Tensor memory: S_0 | S_1 (128 columns each) | O_0 | O_1.  Per key tile
 // and stage: S = Q K^T; the stage's four warps, one thread a row, turn S into P (bf16,
 // over S's own columns, the A operand of the next product); O += P V.  The two stages
@@ -28,9 +29,7 @@
 //
 // Every wait is time-bounded (PARK_ERR_TIMEOUT); on a failed wait the roles leave their
 // loops, copies and MMAs in flight are waited for and TMEM is freed.
-#include "dense.cuh"
-#include "kernels.h"
-#include "sm100.cuh"
+#include "dense_tc.cuh"
 
 namespace park {
 
@@ -38,56 +37,21 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kTile = 128;             // keys of a tile, query rows of a stage
-constexpr uint32_t kPanel = 16384;     // 128 rows of 64 bf16
 constexpr float kRescale = 8.f;        // log2 units
-constexpr int kClean = 4;              // V tiles that the ring can hold at once, at most
 
 template <int NP>
 struct FwdCfg {  // NP: 64-column panels of the padded head dimension
-    static constexpr int ST = NP == 2 ? 5 : 8;  // ring stages (K and V tiles)
+    static constexpr int KS = NP == 2 ? 3 : 4, VS = NP == 2 ? 2 : 4;  // ring stages of K, of V
     static constexpr uint32_t tile = NP * kPanel;
-    static constexpr size_t smem = (size_t)(2 + ST) * tile + 1024;
+    static constexpr size_t smem = (size_t)(2 + KS + VS) * tile + 1024;
 };
 
 struct FwdSmem {
-    uint64_t q_full[2], kv_full[8], kv_empty[8], v_clean[kClean], s_full[2], p_full[2][2], o_full[2], final_bar;
+    uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_clean[4], v_empty[4], s_full[2], p_full[2][2], o_full[2], final_bar;
     uint32_t tmem_base;
     int abort, poison;
     SeqTile seq;
 };
-
-__device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int n, int h, int b) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
-        : "memory");
-}
-// a 16-byte piece with an infinity or NaN among its bf16
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
 struct Piece {
@@ -122,7 +86,8 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ FwdSmem sh;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
     uint8_t* Qs = base;                 // two tiles
-    uint8_t* Ks = base + 2 * C::tile;   // ring
+    uint8_t* Ks = base + 2 * C::tile;   // rings
+    uint8_t* Vs = Ks + C::KS * C::tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
     if (warp == 0) {
@@ -136,11 +101,15 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_init(&sh.p_full[s][1], 128);
                 mbar_init(&sh.o_full[s], 1);
             }
-            for (int s = 0; s < C::ST; ++s) {
-                mbar_init(&sh.kv_full[s], 1);
-                mbar_init(&sh.kv_empty[s], 1);
+            for (int s = 0; s < C::KS; ++s) {
+                mbar_init(&sh.k_full[s], 1);
+                mbar_init(&sh.k_empty[s], 1);
             }
-            for (int s = 0; s < kClean; ++s) mbar_init(&sh.v_clean[s], 1);
+            for (int s = 0; s < C::VS; ++s) {
+                mbar_init(&sh.v_full[s], 1);
+                mbar_init(&sh.v_clean[s], 1);
+                mbar_init(&sh.v_empty[s], 1);
+            }
             mbar_init(&sh.final_bar, 1);
             sh.abort = 0;
             sh.poison = 0;
@@ -167,29 +136,32 @@ __global__ void __launch_bounds__(384, 1)
             // ---------------------------------------------------------------- TMA
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
-            int issued = 0;
-            bool ok = true;
-            for (int i = 0; i < 2 * pc.jmax && ok; ++i) {  // K_0 V_0 K_1 V_1 ...
-                const int st = i % C::ST, round = i / C::ST;
-                if (round > 0 && !mbar_wait(&sh.kv_empty[st], (round - 1) & 1, abort, wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                mbar_arrive_expect_tx(&sh.kv_full[st], C::tile);
-                const int n = t.k0 + (pc.j_lo + (i >> 1)) * kTile;
+            int nk = 0, nv = 0;  // tiles issued
+            for (int j = 0; j < pc.jmax; ++j) {
+                const int n = t.k0 + (pc.j_lo + j) * kTile;
+                const int ks = j % C::KS, vs = j % C::VS;
+                if (j >= C::KS && !mbar_wait(&sh.k_empty[ks], (j / C::KS - 1) & 1, abort, wait_ns)) break;
+                mbar_arrive_expect_tx(&sh.k_full[ks], C::tile);
                 for (int p = 0; p < NP; ++p)
-                    tma_load_4d(Ks + st * C::tile + p * kPanel, i & 1 ? &tmV : &tmK, &sh.kv_full[st], 64 * p, n, hk, b);
-                ++issued;
+                    tma_load_4d(Ks + ks * C::tile + p * kPanel, &tmK, &sh.k_full[ks], 64 * p, n, hk, b);
+                ++nk;
+                if (j >= C::VS && !mbar_wait(&sh.v_empty[vs], (j / C::VS - 1) & 1, abort, wait_ns)) break;
+                mbar_arrive_expect_tx(&sh.v_full[vs], C::tile);
+                for (int p = 0; p < NP; ++p)
+                    tma_load_4d(Vs + vs * C::tile + p * kPanel, &tmV, &sh.v_full[vs], 64 * p, n, hk, b);
+                ++nv;
             }
             int dummy = 0;  // copies in flight land before the CTA may exit
-            for (int i = max(0, issued - C::ST); i < issued; ++i)
-                mbar_wait(&sh.kv_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
+            for (int j = max(0, nk - C::KS); j < nk; ++j)
+                mbar_wait(&sh.k_full[j % C::KS], (j / C::KS) & 1, &dummy, 100000000ull);
+            for (int j = max(0, nv - C::VS); j < nv; ++j)
+                mbar_wait(&sh.v_full[j % C::VS], (j / C::VS) & 1, &dummy, 100000000ull);
         } else if (warp == 9 && lane == 0) {
             // ---------------------------------------------------------------- MMA
             const uint32_t idS = idesc_bf16(128, 128, 0, 0), idO = idesc_bf16(128, 64 * NP, 0, 1);
             auto issue_S = [&](int s, int j) -> bool {
-                const int i = 2 * j, st = i % C::ST;
-                if (!mbar_wait(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
+                const int st = j % C::KS;
+                if (!mbar_wait(&sh.k_full[st], (j / C::KS) & 1, abort, wait_ns)) return false;
                 tc_fence_after();
                 const uint32_t qa = smem_u32(Qs) + s * C::tile, ka = smem_u32(Ks) + st * C::tile;
 #pragma unroll
@@ -200,7 +172,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 umma_commit(&sh.s_full[s]);
                 // the last stage that uses K_j frees it
-                if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.kv_empty[st]);
+                if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.k_empty[st]);
                 return true;
             };
             bool ok = true;
@@ -213,9 +185,9 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
             for (int j = 0; j < pc.jmax && ok; ++j) {
-                const int i = 2 * j + 1, st = i % C::ST;
-                const uint32_t va = smem_u32(Ks) + st * C::tile;
-                if (!mbar_wait(&sh.v_clean[j % kClean], (j / kClean) & 1, abort, wait_ns)) break;
+                const int st = j % C::VS;
+                const uint32_t va = smem_u32(Vs) + st * C::tile;
+                if (!mbar_wait(&sh.v_clean[st], (j / C::VS) & 1, abort, wait_ns)) break;
                 for (int s = 0; s < 2 && ok; ++s) {
                     if (j >= pc.nt[s]) continue;
 #pragma unroll
@@ -232,7 +204,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     if (!ok) break;
                     if (j + 1 == pc.nt[s]) umma_commit(&sh.o_full[s]);
-                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.kv_empty[st]);
+                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.v_empty[st]);
                     if (j + 1 < pc.nt[s]) ok = issue_S(s, j + 1);
                 }
             }
@@ -242,29 +214,20 @@ __global__ void __launch_bounds__(384, 1)
         } else if (warp == 10) {
             // ---------------------------------------------------------------- V tiles: forward, clean where cut
             for (int j = 0; j < pc.jmax; ++j) {
-                const int i = 2 * j + 1, st = i % C::ST;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns))) break;
+                const int st = j % C::VS;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sh.v_full[st], (j / C::VS) & 1, abort, wait_ns))) break;
                 if (j >= cut) {
                     const int n0 = (pc.j_lo + j) * kTile;
-                    uint4* v = reinterpret_cast<uint4*>(Ks + st * C::tile);
+                    uint4* v = reinterpret_cast<uint4*>(Vs + st * C::tile);
                     for (int e = lane; e < (int)(C::tile / 16); e += 32) {
-                        uint4 w = v[e];
-                        if (nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w)) {
-                            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint32_t f = nonfinite2(u[x]);
-                                u[x] &= ~(((f >> 15) & 0x00010001u) * 0xFFFFu);
-                            }
-                            v[e] = w;
-                            if (n0 + (e >> 3) % kTile < t.nk) sh.poison = 1;  // (128 rows of 8 pieces to a panel)
-                        }
+                        // (128 rows of 8 pieces to a panel; rows behind the last key poison nothing)
+                        if (clean16(v + e) && n0 + (e >> 3) % kTile < t.nk) sh.poison = 1;
                     }
                     fence_proxy_async_smem();
                     __threadfence_block();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.v_clean[j % kClean]);
+                if (lane == 0) mbar_arrive(&sh.v_clean[st]);
             }
         }
         __syncwarp();
@@ -478,16 +441,6 @@ __global__ void __launch_bounds__(256)
                 make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
         if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
     }
-}
-
-// 4-D map [B][H][N][D], boxes of 64 x box_rows, 128-byte swizzle; what lies past D or N reads as 0.
-int map_4d(CUtensorMap* m, const Op4& op, int B, int H, long long N, int D, int box_rows) {
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
-    // strides of axes of length 1 are never used: any valid value does
-    const cuuint64_t st[3] = {(cuuint64_t)(N > 1 ? op.sn * 2 : 256), (cuuint64_t)(H > 1 ? op.sh * 2 : 256),
-                              (cuuint64_t)(B > 1 ? op.sb * 2 : 256)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-    return make_tma_map_4d(m, op.p, dims, st, box);
 }
 
 template <int NP>

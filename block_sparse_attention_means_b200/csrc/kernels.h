@@ -213,12 +213,13 @@ int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const
 // ---- k_dense.cu: dense attention (bounds and operands as in dense.cuh)
 struct DenseArgs;
 int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st);
-int launch_dense_fwd_simt(const DenseArgs& a, int dtype, cudaStream_t st);
-int launch_dense_bwd_simt(const DenseArgs& a, int dtype, const float* delta, cudaStream_t st);
+int launch_dense_fwd_simt(const DenseArgs& a, cudaStream_t st);  // float32
+int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st);
 // ---- k_dense_tc.cu: bf16 on tcgen05
 struct DenseSplit;
 DenseSplit dense_split(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D);
 int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st);
+int launch_dense_bwd_tc(const DenseArgs& a, float* delta, cudaStream_t st);  // k_dense_bwd_tc.cu; corrects delta
 int make_tma_map_4d(CUtensorMap* map, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
                     const cuuint32_t* box);
 

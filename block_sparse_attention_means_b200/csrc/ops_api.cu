@@ -245,7 +245,7 @@ int park_attention(const park_attn_shape* shape, const park_operand* q, const pa
     if (s->Nq == 0) return PARK_OK;
     const DenseArgs a = dense_args(s, q, k, v, o, lse, status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return s->dtype == PARK_BF16 ? launch_dense_fwd_tc(a, ws, st) : launch_dense_fwd_simt(a, s->dtype, st);
+    return s->dtype == PARK_BF16 ? launch_dense_fwd_tc(a, ws, st) : launch_dense_fwd_simt(a, st);
 }
 
 int park_attention_bwd(const park_attn_shape* shape, const park_operand* d_o, const park_operand* q,
@@ -275,7 +275,7 @@ int park_attention_bwd(const park_attn_shape* shape, const park_operand* d_o, co
     float* delta = static_cast<float*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s->Nq > 0) PARK_CHECK(launch_dense_delta(a, s->dtype, delta, st));
-    return launch_dense_bwd_simt(a, s->dtype, delta, st);
+    return s->dtype == PARK_BF16 ? launch_dense_bwd_tc(a, delta, st) : launch_dense_bwd_simt(a, delta, st);
 }
 
 }  // extern "C"

@@ -18,6 +18,7 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 E = 2.0 ** -24
+TINY = 2.0 ** -126   # probabilities below the smallest normal number are flushed to 0
 U = {BF: 2.0 ** -8, F32: 2.0 ** -24}
 
 
@@ -376,6 +377,9 @@ def attn_check(q, k, v, got, lse, causal, scale, dt, do=None, grads=None, cu=Non
                 edel = (g.abs() * tol_o).sum(1, keepdim=True) + (D + 4) * E * (g * o).abs().sum(1, keepdim=True)
                 eds = rp * ds.abs() + p * (1 + rp) * (edp + edel) + (up + 4 * E) * ds.abs()
                 eds = eds + up * p * (edp + edel)
+                # a p below 2^-126 becomes 0, in either type's exponent range: off by less than 2^-126 for each
+                # pair, which the relative terms above do not count (they scale with p)
+                eds = eds + torch.where(see, TINY * (dp.abs() + delta.abs()), 0.0)
                 dq = scale * ds @ kk
                 n_k = kk.shape[0]
                 tol = u * dq.abs() + abs(scale) * (eds @ kk.abs() + (n_k + 4) * E * (ds.abs() @ kk.abs())) + 1e-37
@@ -384,7 +388,7 @@ def attn_check(q, k, v, got, lse, causal, scale, dt, do=None, grads=None, cu=Non
                 dv += p.T @ g
                 n_q = qq.shape[0] * (Hq // Hk)
                 tk += abs(scale) * (eds.T @ qq.abs() + (n_q + 4) * E * (ds.abs().T @ qq.abs()))
-                tv += ((rp + up) * p).T @ g.abs() + (n_q + 4) * E * (p.T @ g.abs())
+                tv += ((rp + up) * p + TINY * see).T @ g.abs() + (n_q + 4) * E * (p.T @ g.abs())
             if do is not None:
                 within(grads[1][b, hk, rk], dk, u * dk.abs() + tk + 1e-37, f"dk {b} {hk} {rk}")
                 within(grads[2][b, hk, rk], dv, u * dv.abs() + tv + 1e-37, f"dv {b} {hk} {rk}")
@@ -696,3 +700,16 @@ def test_dense_attention_equals_the_sparse_layer_with_every_block_kept():
         _, p, _, o = plain_attention(q[0, h].double(), k[0, h].double(), v[0, h].double(), D ** -0.5, False)
         tol = 2 * U[BF] * (o.abs() + p @ v[0, h].double().abs()) * 1.05
         assert ((sparse[0, h].double() - dense[0, h].double()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("G", [1, 3])
+def test_single_rows_over_long_keys(G):
+    """The split over the keys at its usual lengths, first call on new memory and again."""
+    lk = [30000, 1, 17777, 257, 4096]
+    q, k, v, _ = attn_inputs(1, 4 * G, 4, len(lk), sum(lk), 128, BF, "tokens", seed=600)
+    kw = dict(cu_q=cu_of([1] * len(lk)), cu_k=cu_of(lk), causal=True)
+    first, lse = park.attention(q, k, v, return_lse=True, **kw)
+    attn_check(q, k, v, first, lse, True, 128 ** -0.5, BF, cu=(kw["cu_q"].tolist(), kw["cu_k"].tolist()))
+    for _ in range(20):
+        k = k.clone()
+        assert torch.equal(park.attention(q, k, v, **kw), first)
