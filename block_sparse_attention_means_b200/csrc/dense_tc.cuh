@@ -41,6 +41,57 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
         : "memory");
 }
+// Time-bounded wait for the phase of the given parity, as mbar_wait but counting SM cycles
+// (at most 2 for each ns of the limit): reading the global timer costs more than most of these waits.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if ((uint64_t)(clock64() - t0) > 2 * limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+// Warp index as a value that the compiler knows to be the same in all lanes.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+// True in one lane of a converged warp, always the same one.  The MMA warp runs its loop with all lanes and
+// issues under this predicate: its operands then live in uniform registers.  Issued from an
+// `if (lane == 0)` branch, each tcgen05.mma waited for their transfer and took about 95 cycles instead of
+// the 64 that a 128 x 128 x 16 product needs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// wait_bar by a whole warp
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, limit_ns));
+}
+// Value of lane `src`'s pointer.
+__device__ __forceinline__ uint8_t* shfl_ptr(uint8_t* p, int src) {
+    return reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
+}
+// 2^x of a pair on the FMA pipe: x = n + r with n the nearest integer (from the low bits of x + 1.5 2^23)
+// and |r| <= 1/2, 2^r by its minimax polynomial of degree 4 in relative error (Remez exchange, 2^-18.5;
+// P is rounded to 2^-8 next), times 2^n.  x <= 128 here; below -127 the factor 2^n is 0.  NaN stays NaN.
+__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
+    const float2 t = __fadd2_rn(x, magic);
+    const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+    const float2 r = __fadd2_rn(x, make_float2(-n.x, -n.y));
+    float2 p = __ffma2_rn(r, make_float2(0.009570102207f, 0.009570102207f), make_float2(0.05591785908f, 0.05591785908f));
+    p = __ffma2_rn(p, r, make_float2(0.2402474433f, 0.2402474433f));
+    p = __ffma2_rn(p, r, make_float2(0.6931217909f, 0.6931217909f));
+    p = __ffma2_rn(p, r, make_float2(0.9999992847f, 0.9999992847f));
+    const float2 e = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3F800000u),
+                                 __uint_as_float((__float_as_uint(t.y) << 23) + 0x3F800000u));
+    return __fmul2_rn(p, e);
+}
 // a 16-byte piece with an infinity or NaN among its bf16
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(384, 1)
         set_status(a.status, PARK_ERR_CUDA);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
     if (warp == 0) {
         const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, kTile, false, 1);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(384, 1)
             int issued = 0;
             for (int i = 0; i < 2 * nt; ++i) {  // K_0 V_0 K_1 V_1 ...
                 const int st = i % C::ST, round = i / C::ST;
-                if (round > 0 && !mbar_wait(&sh.kv_empty[st], (round - 1) & 1, abort, wait_ns)) break;
+                if (round > 0 && !wait_bar(&sh.kv_empty[st], (round - 1) & 1, abort, wait_ns)) break;
                 mbar_arrive_expect_tx(&sh.kv_full[st], C::tile);
                 for (int p = 0; p < NP; ++p)
                     tma_load_4d(ring + st * C::tile + p * kPanel, i & 1 ? &tmV : &tmK, &sh.kv_full[st], 64 * p,
@@ -137,47 +137,57 @@ __global__ void __launch_bounds__(384, 1)
                 ++issued;
             }
             int dummy = 0;  // copies in flight land before the CTA may exit
-            mbar_wait(&sh.own_full, 0, &dummy, 100000000ull);
+            wait_bar(&sh.own_full, 0, &dummy, 100000000ull);
             for (int i = max(0, issued - C::ST); i < issued; ++i)
-                mbar_wait(&sh.kv_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
-        } else if (warp == 9 && lane == 0) {
+                wait_bar(&sh.kv_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
+        } else if (warp == 9) {
             const uint32_t idS = idesc_bf16(128, 128, 0, 0), idQ = idesc_bf16(128, 64 * NP, 0, 1);
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dA[2] = {sdesc_sw128(smem_u32(Qs), 16, 1024), sdesc_sw128(smem_u32(Gs), 16, 1024)};
+            const uint64_t dB = sdesc_sw128(smem_u32(ring), 16, 1024), dBt = sdesc_sw128(smem_u32(ring), kPanel, 1024);
             // w = 0: S of tile j = Q K^T; w = 1: dP = dO V^T
             auto issue_s = [&](int j, int w) -> bool {
                 const int i = 2 * j + w, st = i % C::ST;
-                if (!mbar_wait(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
+                if (!wait_warp(&sh.kv_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
                 tc_fence_after();
-                const uint32_t aa = smem_u32(w ? Gs : Qs), ba = smem_u32(ring) + st * C::tile;
+                const uint64_t ba = dB + ((st * C::tile) >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 4 * NP; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    umma_bf16(tmem + 128 * w, sdesc_sw128(aa + off, 16, 1024), sdesc_sw128(ba + off, 16, 1024), idS,
-                              kk > 0);
+                    for (int kk = 0; kk < 4 * NP; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                        umma_bf16(tm + 128 * w, dA[w] + off, ba + off, idS, kk > 0);
+                    }
+                    if (w) umma_commit(&sh.kv_empty[st]);  // V_j is read once
+                    umma_commit(w ? &sh.dp_full : &sh.s_full);
                 }
-                if (w) umma_commit(&sh.kv_empty[st]);  // V_j is read once
-                umma_commit(w ? &sh.dp_full : &sh.s_full);
+                __syncwarp();
                 return true;
             };
             // w = 0: B += P K; w = 1: dQ += dS K
             auto issue_g = [&](int j, int w) -> bool {
-                if (!mbar_wait(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
+                if (!wait_warp(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
                 tc_fence_after();
                 const int st = (2 * j) % C::ST;
-                const uint32_t ka = smem_u32(ring) + st * C::tile;
+                const uint64_t ka = dBt + ((st * C::tile) >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_bf16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
-                                 sdesc_sw128(ka + kk * 2048, kPanel, 1024), idQ, j > 0 || kk > 0);
-                if (w) umma_commit(&sh.kv_empty[st]);
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
+                                     ka + ((kk * 2048) >> 4), idQ, j > 0 || kk > 0);
+                    if (w) umma_commit(&sh.kv_empty[st]);
+                }
+                __syncwarp();
                 return true;
             };
-            bool ok = nt > 0 && mbar_wait(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
+            bool ok = nt > 0 && wait_warp(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
             for (int j = 0; j < nt && ok; ++j)
                 ok = issue_g(j, 0) && (j + 1 >= nt || issue_s(j + 1, 0)) && issue_g(j, 1) &&
                      (j + 1 >= nt || issue_s(j + 1, 1));
-            umma_commit(&sh.final_bar);
+            if (lead) umma_commit(&sh.final_bar);
+            __syncwarp();
             int dummy = 0;
-            mbar_wait(&sh.final_bar, 0, &dummy, 100000000ull);
+            wait_bar(&sh.final_bar, 0, &dummy, 100000000ull);
         }
         __syncwarp();
     } else {
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(384, 1)
         float2 r2 = make_float2(0.f, 0.f), rb2 = make_float2(0.f, 0.f);  // sums of ds: exact, rounded
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full, j & 1, abort, wait_ns))) {
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(384, 1)
                     pk[e] &= (2 * e <= lim ? 0x0000FFFFu : 0u) | (2 * e + 1 <= lim ? 0xFFFF0000u : 0u);
                 // K_j, which S has been formed from, is cleaned for the sums over its rows
                 const int st = (2 * j) % C::ST;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sh.kv_full[st], ((2 * j) / C::ST) & 1, abort, wait_ns))) {
+                if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_full[st], ((2 * j) / C::ST) & 1, abort, wait_ns))) {
                     ok = false;
                     break;
                 }
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(384, 1)
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sh.p_full);
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.dp_full, j & 1, abort, wait_ns))) {
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
@@ -269,7 +279,7 @@ __global__ void __launch_bounds__(384, 1)
         sh.sum[hc][0][row] = r2.x + r2.y;
         sh.sum[hc][1][row] = rb2.x + rb2.y;
         named_bar_sync(1, 256);
-        if (nt > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.final_bar, 0, abort, wait_ns)) && !__any_sync(0xffffffffu, *abort != 0);
+        if (nt > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&sh.final_bar, 0, abort, wait_ns)) && !__any_sync(0xffffffffu, *abort != 0);
         if (ok) {
             tc_fence_after();
             const float r = sh.sum[0][1][row] + sh.sum[1][1][row];
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(384, 1)
         set_status(a.status, PARK_ERR_CUDA);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
     if (warp == 0) {
         const SeqTile t = dense_resolve(a, blockIdx.x, kTile, true, 1);
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(384, 1)
             int issued = 0, head = hk * G, it = first;
             for (int i = 0; i < 2 * steps; ++i) {  // Q_0 dO_0 Q_1 dO_1 ...
                 const int st = i % C::ST, round = i / C::ST;
-                if (round > 0 && !mbar_wait(&sh.in_empty[st], (round - 1) & 1, abort, wait_ns)) break;
+                if (round > 0 && !wait_bar(&sh.in_empty[st], (round - 1) & 1, abort, wait_ns)) break;
                 mbar_arrive_expect_tx(&sh.in_full[st], C::tile);
                 for (int p = 0; p < NP; ++p)
                     tma_load_4d(ring + st * C::tile + p * kPanel, i & 1 ? &tmG : &tmQ, &sh.in_full[st], 64 * p,
@@ -393,54 +403,64 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             int dummy = 0;
-            mbar_wait(&sh.own_full, 0, &dummy, 100000000ull);
+            wait_bar(&sh.own_full, 0, &dummy, 100000000ull);
             for (int i = max(0, issued - C::ST); i < issued; ++i)
-                mbar_wait(&sh.in_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
-        } else if (warp == 9 && lane == 0) {
+                wait_bar(&sh.in_full[i % C::ST], (i / C::ST) & 1, &dummy, 100000000ull);
+        } else if (warp == 9) {
             const uint32_t idS = idesc_bf16(128, 128, 0, 0), idG = idesc_bf16(128, 64 * NP, 0, 1);
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dA[2] = {sdesc_sw128(smem_u32(Ks), 16, 1024), sdesc_sw128(smem_u32(Vs), 16, 1024)};
+            const uint64_t dB = sdesc_sw128(smem_u32(ring), 16, 1024), dBt = sdesc_sw128(smem_u32(ring), kPanel, 1024);
             // w = 0: S^T of step j = K Q^T; w = 1: dP^T = V dO^T
             auto issue_s = [&](int j, int w) -> bool {
                 const int i = 2 * j + w, st = i % C::ST;
-                if (!mbar_wait(&sh.in_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
+                if (!wait_warp(&sh.in_full[st], (i / C::ST) & 1, abort, wait_ns)) return false;
                 tc_fence_after();
-                const uint32_t aa = smem_u32(w ? Vs : Ks), ba = smem_u32(ring) + st * C::tile;
+                const uint64_t ba = dB + ((st * C::tile) >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 4 * NP; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    umma_bf16(tmem + 128 * w, sdesc_sw128(aa + off, 16, 1024), sdesc_sw128(ba + off, 16, 1024), idS,
-                              kk > 0);
+                    for (int kk = 0; kk < 4 * NP; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                        umma_bf16(tm + 128 * w, dA[w] + off, ba + off, idS, kk > 0);
+                    }
+                    umma_commit(w ? &sh.dp_full : &sh.s_full);
                 }
-                umma_commit(w ? &sh.dp_full : &sh.s_full);
+                __syncwarp();
                 return true;
             };
             // w = 0: dV += P^T dO; w = 1: dK += dS^T Q
             auto issue_g = [&](int j, int w) -> bool {
-                if (!mbar_wait(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
+                if (!wait_warp(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
                 tc_fence_after();
                 const int st = (2 * j + 1 - w) % C::ST;
-                const uint32_t ba = smem_u32(ring) + st * C::tile;
+                const uint64_t ba = dBt + ((st * C::tile) >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_bf16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
-                                 sdesc_sw128(ba + kk * 2048, kPanel, 1024), idG, j > 0 || kk > 0);
-                umma_commit(&sh.in_empty[st]);
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
+                                     ba + ((kk * 2048) >> 4), idG, j > 0 || kk > 0);
+                    umma_commit(&sh.in_empty[st]);
+                }
+                __syncwarp();
                 return true;
             };
-            bool ok = steps > 0 && mbar_wait(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
+            bool ok = steps > 0 && wait_warp(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
             for (int j = 0; j < steps && ok; ++j) {
                 ok = issue_g(j, 0) && (j + 1 >= steps || issue_s(j + 1, 0)) && issue_g(j, 1) &&
                      (j + 1 >= steps || issue_s(j + 1, 1));
             }
-            umma_commit(&sh.final_bar);
+            if (lead) umma_commit(&sh.final_bar);
+            __syncwarp();
             int dummy = 0;
-            mbar_wait(&sh.final_bar, 0, &dummy, 100000000ull);
+            wait_bar(&sh.final_bar, 0, &dummy, 100000000ull);
         } else if (warp == 10) {
             // lse and delta of each step's 128 rows
             const float INF = __int_as_float(0x7f800000);
             int head = hk * G, it = first;
             for (int j = 0; j < steps; ++j) {
                 const int st = j & 1, round = j >> 1;
-                if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.stat_empty[st], (round - 1) & 1, abort, wait_ns))) break;
+                if (round > 0 && !__all_sync(0xffffffffu, wait_bar(&sh.stat_empty[st], (round - 1) & 1, abort, wait_ns))) break;
                 const size_t at = ((size_t)b * a.Hq + head) * a.Nq + t.q0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -469,8 +489,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1, i0 = it * kTile;
             if (++it == end) it = first;
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.stat_full[st], (j >> 1) & 1, abort, wait_ns) &&
-                                             mbar_wait(&sh.s_full, j & 1, abort, wait_ns))) {
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.stat_full[st], (j >> 1) & 1, abort, wait_ns) &&
+                                             wait_bar(&sh.s_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
@@ -508,9 +528,9 @@ __global__ void __launch_bounds__(384, 1)
                              (2 * e + 1 >= lo && 2 * e + 1 <= hi ? 0xFFFF0000u : 0u);
                 // S and dP have been formed from Q and dO: now they are cleaned for the sums over their rows
                 const int sq = (2 * j) % C::ST, sg = (2 * j + 1) % C::ST;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sh.dp_full, j & 1, abort, wait_ns) &&
-                                                 mbar_wait(&sh.in_full[sq], ((2 * j) / C::ST) & 1, abort, wait_ns) &&
-                                                 mbar_wait(&sh.in_full[sg], ((2 * j + 1) / C::ST) & 1, abort, wait_ns))) {
+                if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns) &&
+                                                 wait_bar(&sh.in_full[sq], ((2 * j) / C::ST) & 1, abort, wait_ns) &&
+                                                 wait_bar(&sh.in_full[sg], ((2 * j + 1) / C::ST) & 1, abort, wait_ns))) {
                     ok = false;
                     break;
                 }
@@ -526,7 +546,7 @@ __global__ void __launch_bounds__(384, 1)
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sh.p_full);
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.dp_full, j & 1, abort, wait_ns))) {
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_before();
             mbar_arrive(&sh.ds_full);
         }
-        if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.final_bar, 0, abort, wait_ns)) && !__any_sync(0xffffffffu, *abort != 0);
+        if (steps > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&sh.final_bar, 0, abort, wait_ns)) && !__any_sync(0xffffffffu, *abort != 0);
         if (ok) {
             tc_fence_after();
             const bool live = row < keys;

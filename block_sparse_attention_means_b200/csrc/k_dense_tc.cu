@@ -53,6 +53,11 @@ struct FwdSmem {
     SeqTile seq;
 };
 
+#ifndef POLY
+#define POLY 2
+#endif
+__device__ constexpr bool poly_pair(int e) { return (e * POLY) % 8 < POLY; }
+
 // The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
 struct Piece {
     int r0, rows, nt[2], j_lo, jmax;
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t* Qs = base;                 // two tiles
     uint8_t* Ks = base + 2 * C::tile;   // rings
     uint8_t* Vs = Ks + C::KS * C::tile;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
     if (warp == 0) {
         const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, 2 * kTile, false, a.Hq / a.Hk);
@@ -140,12 +145,12 @@ __global__ void __launch_bounds__(384, 1)
             for (int j = 0; j < pc.jmax; ++j) {
                 const int n = t.k0 + (pc.j_lo + j) * kTile;
                 const int ks = j % C::KS, vs = j % C::VS;
-                if (j >= C::KS && !mbar_wait(&sh.k_empty[ks], (j / C::KS - 1) & 1, abort, wait_ns)) break;
+                if (j >= C::KS && !wait_bar(&sh.k_empty[ks], (j / C::KS - 1) & 1, abort, wait_ns)) break;
                 mbar_arrive_expect_tx(&sh.k_full[ks], C::tile);
                 for (int p = 0; p < NP; ++p)
                     tma_load_4d(Ks + ks * C::tile + p * kPanel, &tmK, &sh.k_full[ks], 64 * p, n, hk, b);
                 ++nk;
-                if (j >= C::VS && !mbar_wait(&sh.v_empty[vs], (j / C::VS - 1) & 1, abort, wait_ns)) break;
+                if (j >= C::VS && !wait_bar(&sh.v_empty[vs], (j / C::VS - 1) & 1, abort, wait_ns)) break;
                 mbar_arrive_expect_tx(&sh.v_full[vs], C::tile);
                 for (int p = 0; p < NP; ++p)
                     tma_load_4d(Vs + vs * C::tile + p * kPanel, &tmV, &sh.v_full[vs], 64 * p, n, hk, b);
@@ -153,69 +158,79 @@ __global__ void __launch_bounds__(384, 1)
             }
             int dummy = 0;  // copies in flight land before the CTA may exit
             for (int j = max(0, nk - C::KS); j < nk; ++j)
-                mbar_wait(&sh.k_full[j % C::KS], (j / C::KS) & 1, &dummy, 100000000ull);
+                wait_bar(&sh.k_full[j % C::KS], (j / C::KS) & 1, &dummy, 100000000ull);
             for (int j = max(0, nv - C::VS); j < nv; ++j)
-                mbar_wait(&sh.v_full[j % C::VS], (j / C::VS) & 1, &dummy, 100000000ull);
-        } else if (warp == 9 && lane == 0) {
+                wait_bar(&sh.v_full[j % C::VS], (j / C::VS) & 1, &dummy, 100000000ull);
+        } else if (warp == 9) {
             // ---------------------------------------------------------------- MMA
             const uint32_t idS = idesc_bf16(128, 128, 0, 0), idO = idesc_bf16(128, 64 * NP, 0, 1);
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dQ = sdesc_sw128(smem_u32(Qs), 16, 1024), dK = sdesc_sw128(smem_u32(Ks), 16, 1024);
+            const uint64_t dV = sdesc_sw128(smem_u32(Vs), kPanel, 1024);
             auto issue_S = [&](int s, int j) -> bool {
                 const int st = j % C::KS;
-                if (!mbar_wait(&sh.k_full[st], (j / C::KS) & 1, abort, wait_ns)) return false;
+                if (!wait_warp(&sh.k_full[st], (j / C::KS) & 1, abort, wait_ns)) return false;
                 tc_fence_after();
-                const uint32_t qa = smem_u32(Qs) + s * C::tile, ka = smem_u32(Ks) + st * C::tile;
+                const uint64_t qa = dQ + ((s * C::tile) >> 4), ka = dK + ((st * C::tile) >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 4 * NP; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    umma_bf16(tmem + 128 * s, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idS,
-                              kk > 0);
+                    for (int kk = 0; kk < 4 * NP; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                        umma_bf16(tm + 128 * s, qa + off, ka + off, idS, kk > 0);
+                    }
+                    umma_commit(&sh.s_full[s]);
+                    // the last stage that uses K_j frees it
+                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.k_empty[st]);
                 }
-                umma_commit(&sh.s_full[s]);
-                // the last stage that uses K_j frees it
-                if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.k_empty[st]);
+                __syncwarp();
                 return true;
             };
             bool ok = true;
             for (int s = 0; s < 2 && ok; ++s)
                 if (pc.nt[s] > 0) {
-                    ok = mbar_wait(&sh.q_full[s], 0, abort, wait_ns);
-                    if (ok) {
-                        tc_fence_after();
-                        ok = issue_S(s, 0);
-                    }
+                    ok = wait_warp(&sh.q_full[s], 0, abort, wait_ns);
+                    if (ok) ok = issue_S(s, 0);
                 }
             for (int j = 0; j < pc.jmax && ok; ++j) {
                 const int st = j % C::VS;
-                const uint32_t va = smem_u32(Vs) + st * C::tile;
-                if (!mbar_wait(&sh.v_clean[st], (j / C::VS) & 1, abort, wait_ns)) break;
+                const uint64_t va = dV + ((st * C::tile) >> 4);
+                if (!wait_warp(&sh.v_clean[st], (j / C::VS) & 1, abort, wait_ns)) break;
                 for (int s = 0; s < 2 && ok; ++s) {
                     if (j >= pc.nt[s]) continue;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (!mbar_wait(&sh.p_full[s][h], j & 1, abort, wait_ns)) {
+                        if (!wait_warp(&sh.p_full[s][h], j & 1, abort, wait_ns)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                        if (lead) {
 #pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            umma_bf16_ts(tmem + 256 + 64 * NP * s, tmem + 128 * s + 8 * kk,
-                                         sdesc_sw128(va + kk * 2048, kPanel, 1024), idO, j > 0 || kk > 0);
+                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                umma_bf16_ts(tm + 256 + 64 * NP * s, tm + 128 * s + 8 * kk, va + ((kk * 2048) >> 4), idO,
+                                             j > 0 || kk > 0);
+                        }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    if (j + 1 == pc.nt[s]) umma_commit(&sh.o_full[s]);
-                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.v_empty[st]);
+                    if (lead) {
+                        if (j + 1 == pc.nt[s]) umma_commit(&sh.o_full[s]);
+                        if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.v_empty[st]);
+                    }
+                    __syncwarp();
                     if (j + 1 < pc.nt[s]) ok = issue_S(s, j + 1);
                 }
             }
-            umma_commit(&sh.final_bar);  // every MMA is done before TMEM is released
+            if (lead) umma_commit(&sh.final_bar);  // every MMA is done before TMEM is released
+            __syncwarp();
             int dummy = 0;
-            mbar_wait(&sh.final_bar, 0, &dummy, 100000000ull);
+            wait_bar(&sh.final_bar, 0, &dummy, 100000000ull);
         } else if (warp == 10) {
             // ---------------------------------------------------------------- V tiles: forward, clean where cut
             for (int j = 0; j < pc.jmax; ++j) {
                 const int st = j % C::VS;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sh.v_full[st], (j / C::VS) & 1, abort, wait_ns))) break;
+                if (!__all_sync(0xffffffffu, wait_bar(&sh.v_full[st], (j / C::VS) & 1, abort, wait_ns))) break;
                 if (j >= cut) {
                     const int n0 = (pc.j_lo + j) * kTile;
                     uint4* v = reinterpret_cast<uint4*>(Vs + st * C::tile);
@@ -241,20 +256,23 @@ __global__ void __launch_bounds__(384, 1)
         const int r = pc.r0 + kTile * s + row;
         const int tok = r / G, head = hk * G + (r - tok * G);
         const bool live = kTile * s + row < pc.rows;
+        constexpr int PR = 8 * NP;  // 16-byte pieces of a row
+        uint8_t* qt = Qs + s * C::tile;
+        const int chunks = a.D / 8;
         if (nt > 0) {
-            // the warp's 32 query rows, 8 NP pieces of 16 bytes each, into the swizzled tile
-            constexpr int PR = 8 * NP;
-            uint8_t* qt = Qs + s * C::tile;
-            const int chunks = a.D / 8;
-#pragma unroll 4
-            for (int e = lane; e < 32 * PR; e += 32) {
-                const int rr = 32 * quad + e / PR, c = e % PR;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (kTile * s + rr < pc.rows && c < chunks) {
-                    const int rg = pc.r0 + kTile * s + rr, tk = rg / G, hh = hk * G + (rg - tk * G);
-                    v = __ldg(reinterpret_cast<const uint4*>(a.q.p + (b * a.q.sb + hh * a.q.sh + (t.q0 + tk) * a.q.sn) * 2) + c);
-                }
-                *reinterpret_cast<uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+            // the warp's 32 query rows into the swizzled tile, all loads in flight at once
+            uint8_t* src = live ? a.q.p + (b * a.q.sb + head * a.q.sh + (t.q0 + tok) * a.q.sn) * 2 : nullptr;
+            uint4 v[PR];
+#pragma unroll
+            for (int i = 0; i < PR; ++i) {
+                const int e = 32 * i + lane;
+                const uint8_t* row_src = shfl_ptr(src, e / PR);
+                v[i] = row_src && e % PR < chunks ? __ldg(reinterpret_cast<const uint4*>(row_src) + e % PR) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < PR; ++i) {
+                const int e = 32 * i + lane, rr = 32 * quad + e / PR, c = e % PR;
+                *reinterpret_cast<uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[i];
             }
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full[s]);
@@ -263,10 +281,10 @@ __global__ void __launch_bounds__(384, 1)
         const float2 sl22 = make_float2(sl2, sl2);
         const int seen = live ? dense_last_key(tok, t.nq, t.nk, a.causal) : -1;  // last visible key
         float m = NI;
-        float2 l2 = make_float2(0.f, 0.f);
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[s], j & 1, abort, wait_ns))) {
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
@@ -307,35 +325,40 @@ __global__ void __launch_bounds__(384, 1)
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * f);
                     tmem_st32(ocol + 32 * c, o);
                 }
-                l2.x *= f;
-                l2.y *= f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l2[e] = __fmul2_rn(l2[e], make_float2(f, f));
                 m = mn;
             }
             const float mr = m == NI ? 0.f : m;  // a row that has seen no key yet: P = 0
             const float2 nm = make_float2(-mr, -mr);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
+            for (int h = 0; h < 2; ++h) {  // the MMA warp starts on the first 64 keys while the others follow
+                uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 d = __ffma2_rn(make_float2(f_of(x[c][2 * e]), f_of(x[c][2 * e + 1])), sl22, nm);
-                    const float p0 = ex2(d.x), p1 = ex2(d.y);
-                    l2 = __fadd2_rn(l2, make_float2(p0, p1));
-                    pk[e] = bf2(p0, p1);
+                for (int e = 0; e < 32; ++e) {
+                    const int c = 2 * h + (e >> 4), y = 2 * (e & 15);
+                    const float2 d = __ffma2_rn(make_float2(f_of(x[c][y]), f_of(x[c][y + 1])), sl22, nm);
+                    // some of the exponentials on the FMA pipe, the others on the special-function unit, which alone
+                    // would take as long as the two products
+                    const float2 pe = poly_pair(e) ? ex2_poly2(d) : make_float2(ex2(d.x), ex2(d.y));
+                    l2[e & 1] = __fadd2_rn(l2[e & 1], pe);
+                    pk[e] = bf2(pe.x, pe.y);
                 }
-                tmem_st16(scol + 16 * c, pk);
-                if (c & 1) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive(&sh.p_full[s][c >> 1]);
-                }
+                tmem_st32(scol + 32 * h, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[s][h]);
             }
         }
         // ---------------------------------------------------------------- epilogue
-        float l = l2.x + l2.y;
-        if (nt > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.o_full[s], 0, abort, wait_ns));
+        const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        if (nt > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&sh.o_full[s], 0, abort, wait_ns));
         if (ok) {
             tc_fence_after();
+            int r = pc.r0 + kTile * s + row;  // (formed again: nothing of it has to live through the loop)
+            asm volatile("" : "+r"(r));
+            const int tok = r / G, head = hk * G + (r - tok * G);
+            const bool live = kTile * s + row < pc.rows;
             const bool none = m == NI && l == 0.f;  // no visible key (or every score -inf)
             const float inv = none ? 0.f : 1.f / l;
             const size_t row_id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
@@ -378,13 +401,25 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             *reinterpret_cast<uint4*>(prow + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    } else if (live) {
+                    } else if (!split) {  // through the stage's own Q tile, which no MMA reads any more
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(orow + 2 * (32 * c + e)) =
+                            *reinterpret_cast<uint4*>(qt + (c >> 1) * kPanel + row * 128 +
+                                                      ((((4 * c + (e >> 3)) & 7) ^ (row & 7)) << 4)) =
                                 make_uint4(bf2(f_of(o[e]), f_of(o[e + 1])), bf2(f_of(o[e + 2]), f_of(o[e + 3])),
                                            bf2(f_of(o[e + 4]), f_of(o[e + 5])), bf2(f_of(o[e + 6]), f_of(o[e + 7])));
                     }
+                }
+            }
+            if (!split) {  // whole rows, 16 bytes a lane
+                __syncwarp();
+                uint8_t* dst = live ? orow : nullptr;
+#pragma unroll
+                for (int i = 0; i < PR; ++i) {
+                    const int e = 32 * i + lane, rr = 32 * quad + e / PR, c = e % PR;
+                    uint8_t* row_dst = shfl_ptr(dst, e / PR);
+                    const uint4 v = *reinterpret_cast<const uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+                    if (row_dst && c < chunks) *(reinterpret_cast<uint4*>(row_dst) + c) = v;
                 }
             }
         }
@@ -401,46 +436,40 @@ __global__ void __launch_bounds__(384, 1)
 // Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum; one warp a row.
 __global__ void __launch_bounds__(256)
     k_dense_combine(DenseArgs a, int n_split, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
-    __shared__ SeqTile sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
-    if (warp == 0) {
-        const SeqTile t = dense_resolve(a, blockIdx.x, 2 * kTile, false, G);
-        if (lane == 0) sh = t;
-    }
-    __syncthreads();
-    const SeqTile t = sh;
+    const int lane = threadIdx.x & 31, G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
+    const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (x >= a.Nq * G) return;
+    const SeqTile t = dense_resolve(a, x, 1, false, G);  // tiles of one row
     if (!t.live) return;
+    const float NI = __int_as_float(0xff800000);
     const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
-    const int r1 = min(t.nq * G, (t.tile + 1) * 2 * kTile);
-    for (int r = t.tile * 2 * kTile + warp; r < r1; r += 8) {
-        const int tok = r / G, head = hk * G + (r - tok * G);
-        const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
-        float M = __int_as_float(0xff800000);
-        for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
-        M = warp_max(M);
-        const bool none = M == __int_as_float(0xff800000);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        for (int s = 0; s < n_split; ++s) {
-            const float ls = part_lse[s * rows_all + id];
-            if (ls == __int_as_float(0xff800000)) continue;  // (its part of o may not be written)
-            const float w = ex2(ls - M);
-            sum += w;
-            if (4 * lane < a.D) {
-                const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
-                acc.x = fmaf(w, o.x, acc.x);
-                acc.y = fmaf(w, o.y, acc.y);
-                acc.z = fmaf(w, o.z, acc.z);
-                acc.w = fmaf(w, o.w, acc.w);
-            }
+    const int tok = t.tile / G, head = hk * G + (t.tile - tok * G);
+    const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
+    float M = NI;
+    for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
+    M = warp_max(M);
+    const bool none = M == NI;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < n_split; ++s) {
+        const float ls = part_lse[s * rows_all + id];
+        if (ls == NI) continue;  // (its part of o may not be written)
+        const float w = ex2(ls - M);
+        sum += w;
+        if (4 * lane < a.D) {
+            const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
         }
-        const float inv = none ? 0.f : 1.f / sum;
-        if (4 * lane < a.D)
-            *reinterpret_cast<uint2*>(a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2 + 8 * lane) =
-                make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-        if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
     }
+    const float inv = none ? 0.f : 1.f / sum;
+    if (4 * lane < a.D)
+        *reinterpret_cast<uint2*>(a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2 + 8 * lane) =
+            make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
 }
 
 template <int NP>
@@ -491,7 +520,7 @@ int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
                          : fwd_tc<2>(a, mK, mV, sp, part_o, part_lse, st));
     if (sp.n == 1) return PARK_OK;
     ::park::prof_begin(st);
-    k_dense_combine<<<dim3((unsigned)sp.tiles, a.Hk, a.B), 256, 0, st>>>(a, sp.n, part_o, part_lse);
+    k_dense_combine<<<dim3((unsigned)((a.Nq * (a.Hq / a.Hk) + 7) / 8), a.Hk, a.B), 256, 0, st>>>(a, sp.n, part_o, part_lse);
     PARK_TRY_LAUNCH("k_dense_combine", st);
     return PARK_OK;
 }

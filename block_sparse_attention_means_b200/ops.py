@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 
 import torch
@@ -44,7 +45,8 @@ def status_word(device=None) -> torch.Tensor:
     return _status_words[index]
 
 
-def _check(name: str, t: torch.Tensor, shape=None, dtype=None, device=None, output=False) -> None:
+def _check(name: str, t, shape=None, dtype=None, device=None, output=False) -> None:
+    """Says in words what is wrong with a tensor (the library checks the same, as codes)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor [B, H, N, D]")
     if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
@@ -71,51 +73,85 @@ def _check(name: str, t: torch.Tensor, shape=None, dtype=None, device=None, outp
             reach += s * (n - 1)
 
 
-def _op(t: torch.Tensor) -> _lib.ParkOperand:
-    st = [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
-    return _lib.ParkOperand(t.data_ptr(), t.shape[1], st[0], st[1], st[2])
+def _same(x, *others) -> bool:
+    """All on one CUDA device, in one dtype that the library takes, with four axes."""
+    dev, dt = x.get_device(), x.dtype
+    if dev < 0 or dt not in _DT or x.dim() != 4:
+        return False
+    for t in others:
+        if t.get_device() != dev or t.dtype is not dt or t.dim() != 4:
+            return False
+    return True
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+def _op(name: str, t: torch.Tensor) -> _lib.ParkOperand:
+    """The tensor as the library takes it (which checks the pointer and the outer strides)."""
+    shape, st = t.shape, t.stride()
+    if st[3] != 1:
+        _check(name, t)
+    return _lib.ParkOperand(t.data_ptr(), shape[1], st[0], st[1], st[2])
+
+
+def _done(rc: int, what: str, inputs=(), outputs=()) -> None:
+    """Raises for a refused call: in words where a tensor is the cause, else the library's code."""
+    if rc != _lib.PARK_OK:
+        for name, t in inputs:
+            _check(name, t)
+        for name, t in outputs:
+            _check(name, t, output=True)
+        _lib.check(rc, what)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 class _On:
     """Runs a call on the tensors' device and the given (or current) stream, so that
-    memory allocated inside belongs to that stream."""
+    memory allocated inside belongs to that stream; yields the stream's handle."""
+    __slots__ = ("index", "dev", "ctx")
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream on {stream.device}, tensors on {device}")
-        self.dev, self.stream = torch.cuda.device(device), stream
+    def __init__(self, index: int, stream):
+        self.index, self.dev, self.ctx = index, None, None
+        if stream is not None:
+            if stream.device.index != index:
+                raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
+            self.ctx = torch.cuda.stream(stream)
+        if torch.cuda.current_device() != index:
+            self.dev = torch.cuda.device(index)
 
     def __enter__(self):
-        self.dev.__enter__()
-        self.ctx = torch.cuda.stream(self.stream) if self.stream is not None else None
+        if self.dev is not None:
+            self.dev.__enter__()
         if self.ctx is not None:
             self.ctx.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
-        self.dev.__exit__(*exc)
+        if self.dev is not None:
+            self.dev.__exit__(*exc)
 
 
-def _status(status, device) -> torch.Tensor:
+def _status(status, index: int) -> int:
     if status is None:
-        return status_word(device)
-    if status.dtype != torch.int32 or status.numel() != 1 or status.device != device:
+        word = _status_words.get(index)
+        return (status_word(index) if word is None else word).data_ptr()
+    if status.dtype != torch.int32 or status.numel() != 1 or status.get_device() != index:
         raise ValueError("status must be int32 [1] on the tensors' device")
-    return status
+    return status.data_ptr()
 
 
-def _workspace(ws, need: int, device) -> torch.Tensor:
+def _workspace(ws, need: int, like):
+    """(tensor that keeps it alive, pointer, bytes)"""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if not ws.is_contiguous() or ws.device != device:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif not ws.is_contiguous() or ws.get_device() != like.get_device():
         raise ValueError("ws must be contiguous on the tensors' device")
-    return ws
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -129,8 +165,7 @@ class Rope:
 
     def c(self) -> _lib.ParkRopeAxes:
         i3 = ctypes.c_int * 3
-        return _lib.ParkRopeAxes(i3(*self.extent), i3(*self.pairs), int(self.half),
-                                 ctypes.c_void_p(self.table.data_ptr()))
+        return _lib.ParkRopeAxes(i3(*self.extent), i3(*self.pairs), self.half, self.table.data_ptr())
 
 
 def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1.0, 1.0), half: bool = False,
@@ -151,31 +186,37 @@ def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    with _On(dev, stream) as st:
+    with _On(dev.index, stream) as st:
         r = Rope(extent, pairs, bool(half), torch.empty(0, dtype=torch.float32, device=dev))
-        n = _lib.load().park_rope_table_floats(ctypes.byref(r.c()))
+        n = _lib.load().park_rope_table_floats(r.c())
         r.table = torch.empty(max(2, n), dtype=torch.float32, device=dev)
-        rc = _lib.load().park_rope_table(ctypes.byref(r.c()), float(theta),
+        rc = _lib.load().park_rope_table(r.c(), float(theta),
                                          (ctypes.c_double * 3)(*[float(x) for x in scale]), st)
     _lib.check(rc, "park_rope_table")
     return r
 
 
-def _rope_args(rope, positions, B: int, N: int, D: int, device):
+def _rope_args(rope, positions, B: int, N: int, D: int, index: int):
     if rope is None:
         if positions is not None:
             raise ValueError("positions without rope")
-        return None, ctypes.c_void_p(0), 0
-    if rope.table.device != device:
-        raise ValueError(f"rope table on {rope.table.device}, tensors on {device}")
+        return None, None, 0
+    if rope.table.get_device() != index:
+        raise ValueError(f"rope table on {rope.table.device}, tensors on cuda:{index}")
     if sum(rope.pairs) > D // 2:
         raise ValueError(f"rope rotates {sum(rope.pairs)} pairs, the head has {D // 2}")
     if positions is None:
-        return ctypes.byref(rope.c()), ctypes.c_void_p(0), 0
-    if (positions.dtype != torch.int32 or positions.device != device or not positions.is_contiguous()
+        return rope.c(), None, 0
+    if (positions.dtype != torch.int32 or positions.get_device() != index or not positions.is_contiguous()
             or tuple(positions.shape) not in ((N, 3), (B, N, 3))):
-        raise ValueError(f"positions must be contiguous int32 [N, 3] or [B, N, 3] with N = {N} on {device}")
-    return ctypes.byref(rope.c()), _ptr(positions), 3 * N if positions.dim() == 3 else 0
+        raise ValueError(f"positions must be contiguous int32 [N, 3] or [B, N, 3] with N = {N} on cuda:{index}")
+    return rope.c(), positions.data_ptr(), 3 * N if positions.dim() == 3 else 0
+
+
+def _output(name: str, out, like):
+    if not _same(like, out) or out.shape != like.shape:
+        _check(name, out, like.shape, like.dtype, like.device, output=True)
+    return out
 
 
 def rope(x, rope: Rope, positions=None, inverse: bool = False, out=None, status=None, stream=None) -> torch.Tensor:
@@ -183,43 +224,55 @@ def rope(x, rope: Rope, positions=None, inverse: bool = False, out=None, status=
     gradient (dx from dy).  positions: int32 [N, 3] or [B, N, 3] with (t, y, w) of each
     token, negative for text (not rotated); None: the grid order of Shape, tokens behind
     the grid not rotated.  ``out`` may be x."""
-    _check("x", x)
-    B, H, N, D = x.shape
-    with _On(x.device, stream) as st:
-        out = torch.empty_like(x) if out is None else out
-        _check("out", out, x.shape, x.dtype, x.device, output=True)
-        axes, pos, sb = _rope_args(rope, positions, B, N, D, x.device)
-        if axes is None:
-            raise ValueError("rope is missing")
-        rc = _lib.load().park_rope(_op(x), _op(out), B, N, D, _DT[x.dtype], axes, pos, sb, int(inverse),
-                                   _ptr(_status(status, x.device)), st) if B * H else 0
-    _lib.check(rc, "park_rope")
+    if not isinstance(x, torch.Tensor) or not _same(x):
+        _check("x", x)
+    if rope is None:
+        raise ValueError("rope is missing")
+    (B, H, N, D), index = x.shape, x.get_device()
+    with _On(index, stream) as st:
+        out = torch.empty_like(x) if out is None else _output("out", out, x)
+        axes, pos, sb = _rope_args(rope, positions, B, N, D, index)
+        if B * H == 0:
+            return out
+        rc = _lib.load().park_rope(_op("x", x), _op("out", out), B, N, D, _DT[x.dtype], axes, pos, sb, inverse,
+                                   _status(status, index), st)
+    if rc:
+        _done(rc, "park_rope", (("x", x),), (("out", out),))
     return out
 
 
 # ------------------------------------------------------------------ norm + rotation
 def _pair_check(q, k, more=()):
-    _check("q", q)
-    B, _, N, D = q.shape
-    _check("k", k, (B, k.shape[1] if k.dim() == 4 else 0, N, D), q.dtype, q.device)
-    if min(B, q.shape[1], k.shape[1]) < 1:
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or not _same(q, k):
+        _check("q", q)
+        _check("k", k, None, q.dtype, q.device)
+    B, H, N, D = q.shape
+    ks = k.shape
+    if ks[0] != B or ks[2] != N or ks[3] != D:
+        _check("k", k, (B, ks[1], N, D))
+    if min(B, H, ks[1]) < 1:
         raise ValueError("q and k need at least one batch entry and one head")
     for name, t, like in more:
-        _check(name, t, like.shape, q.dtype, q.device)
-    return B, N, D
+        if not _same(like, t) or t.shape != like.shape:
+            _check(name, t, like.shape, q.dtype, q.device)
+    return B, N, D, q.get_device()
 
 
-def _weights(q_weight, k_weight, D: int, device):
+def _weights(q_weight, k_weight, D: int, index: int):
     dt = None
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is None:
             continue
-        if tuple(w.shape) != (D,) or w.dtype not in _DT or not w.is_contiguous() or w.device != device:
-            raise ValueError(f"{name} must be contiguous [D] in bfloat16 or float32 on {device}")
+        if w.shape != (D,) or w.dtype not in _DT or w.stride(0) != 1 or w.get_device() != index:
+            raise ValueError(f"{name} must be contiguous [D] in bfloat16 or float32 on cuda:{index}")
         if dt is not None and w.dtype != dt:
             raise TypeError("q_weight and k_weight have different dtypes")
         dt = w.dtype
     return _ptr(q_weight), _ptr(k_weight), _DT[dt or torch.float32]
+
+
+def _contiguous_like(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope: Rope | None = None, positions=None, eps: float = 1e-6,
@@ -228,18 +281,26 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope: Rope | None = None, p
     weight [D] (None: ones), rotated as by ``rope`` (None: not), in one pass, float32
     inside and rounded once.  q has H heads, k may have fewer.  New outputs are
     contiguous [B, H, N, D], the layout that layer() takes; q_out may be q, k_out k."""
-    B, N, D = _pair_check(q, k)
-    with _On(q.device, stream) as st:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _check("q_out", q_out, q.shape, q.dtype, q.device, output=True)
-        _check("k_out", k_out, k.shape, k.dtype, k.device, output=True)
-        axes, pos, sb = _rope_args(rope, positions, B, N, D, q.device)
-        wq, wk, wdt = _weights(q_weight, k_weight, D, q.device)
-        rc = _lib.load().park_qk_norm_rope(_op(q), _op(k), wq, wk, wdt, float(eps), axes, pos, sb, _op(q_out),
-                                           _op(k_out), B, N, D, _DT[q.dtype], _ptr(_status(status, q.device)), st)
-    _lib.check(rc, "park_qk_norm_rope")
+    B, N, D, index = _pair_check(q, k)
+    with _On(index, stream) as st:
+        q_out = _contiguous_like(q) if q_out is None else _output("q_out", q_out, q)
+        k_out = _contiguous_like(k) if k_out is None else _output("k_out", k_out, k)
+        axes, pos, sb = _rope_args(rope, positions, B, N, D, index)
+        wq, wk, wdt = _weights(q_weight, k_weight, D, index)
+        rc = _lib.load().park_qk_norm_rope(_op("q", q), _op("k", k), wq, wk, wdt, eps, axes, pos, sb,
+                                           _op("q_out", q_out), _op("k_out", k_out), B, N, D, _DT[q.dtype],
+                                           _status(status, index), st)
+    if rc:
+        _done(rc, "park_qk_norm_rope", (("q", q), ("k", k)), (("q_out", q_out), ("k_out", k_out)))
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_workspace(B: int, N: int, D: int) -> int:
+    need = ctypes.c_size_t(0)
+    _lib.check(_lib.load().park_qk_norm_rope_bwd_workspace(B, N, D, ctypes.byref(need)),
+               "park_qk_norm_rope_bwd_workspace")
+    return need.value
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope: Rope | None = None, positions=None,
@@ -247,24 +308,22 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope: R
     """(dq, dk, dq_weight, dk_weight) from the gradients of qk_norm_rope's outputs and its
     own inputs.  dq, dk in the inputs' type; the weights' gradients float32 [D], None
     where there is no weight."""
-    B, N, D = _pair_check(q, k, (("dq_out", dq_out, q), ("dk_out", dk_out, k)))
-    lib = _lib.load()
-    with _On(q.device, stream) as st:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        _check("dq", dq, q.shape, q.dtype, q.device, output=True)
-        _check("dk", dk, k.shape, k.dtype, k.device, output=True)
-        axes, pos, sb = _rope_args(rope, positions, B, N, D, q.device)
-        wq, wk, wdt = _weights(q_weight, k_weight, D, q.device)
-        need = ctypes.c_size_t(0)
-        _lib.check(lib.park_qk_norm_rope_bwd_workspace(B, N, D, ctypes.byref(need)), "park_qk_norm_rope_bwd_workspace")
-        ws = _workspace(ws, need.value, q.device)
+    B, N, D, index = _pair_check(q, k, (("dq_out", dq_out, q), ("dk_out", dk_out, k)))
+    with _On(index, stream) as st:
+        dq = _contiguous_like(q) if dq is None else _output("dq", dq, q)
+        dk = _contiguous_like(k) if dk is None else _output("dk", dk, k)
+        axes, pos, sb = _rope_args(rope, positions, B, N, D, index)
+        wq, wk, wdt = _weights(q_weight, k_weight, D, index)
+        ws, wp, wn = _workspace(ws, _norm_bwd_workspace(B, N, D), q)
         dw = [torch.empty(D, dtype=torch.float32, device=q.device) if w is not None else None
               for w in (q_weight, k_weight)]
-        rc = lib.park_qk_norm_rope_bwd(_op(dq_out), _op(dk_out), _op(q), _op(k), wq, wk, wdt, float(eps), axes, pos, sb,
-                                       _op(dq), _op(dk), _ptr(dw[0]), _ptr(dw[1]), B, N, D, _DT[q.dtype], _ptr(ws),
-                                       ws.numel() * ws.element_size(), _ptr(_status(status, q.device)), st)
-    _lib.check(rc, "park_qk_norm_rope_bwd")
+        rc = _lib.load().park_qk_norm_rope_bwd(
+            _op("dq_out", dq_out), _op("dk_out", dk_out), _op("q", q), _op("k", k), wq, wk, wdt, eps, axes, pos, sb,
+            _op("dq", dq), _op("dk", dk), _ptr(dw[0]), _ptr(dw[1]), B, N, D, _DT[q.dtype], wp, wn,
+            _status(status, index), st)
+    if rc:
+        _done(rc, "park_qk_norm_rope_bwd", (("dq_out", dq_out), ("dk_out", dk_out), ("q", q), ("k", k)),
+              (("dq", dq), ("dk", dk)))
     return dq, dk, dw[0], dw[1]
 
 
@@ -285,8 +344,9 @@ class NormRope:
                                 stream=stream)
         if self.rope is None:
             raise ValueError("NormRope with neither norm nor rope")
-        with _On(q.device, stream):
-            outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
+        _pair_check(q, k)
+        with _On(q.get_device(), stream):
+            outs = [_contiguous_like(t) for t in (q, k)]
         return tuple(rope(t, self.rope, self.positions, out=o, status=status, stream=stream)
                      for t, o in zip((q, k), outs))
 
@@ -294,46 +354,58 @@ class NormRope:
 # ------------------------------------------------------------------ dense attention
 def _attn_shape(q, k, causal, scale, cu_q, cu_k) -> _lib.ParkAttnShape:
     B, _, Nq, D = q.shape
-    Nk, n_seq = k.shape[2], 0
+    n_seq = 0
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k go together")
     if cu_q is not None:
         for name, cu in (("cu_q", cu_q), ("cu_k", cu_k)):
-            if cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous() or cu.device != q.device:
+            if (cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous()
+                    or cu.get_device() != q.get_device()):
                 raise ValueError(f"{name} must be a contiguous int32 vector on {q.device}")
         if cu_q.numel() != cu_k.numel() or cu_q.numel() < 2:
             raise ValueError("cu_q and cu_k hold the sequences' bounds: n_seq + 1 entries each")
         if B != 1:
             raise ValueError("packed sequences need B = 1")
         n_seq = cu_q.numel() - 1
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    return _lib.ParkAttnShape(B, D, _DT[q.dtype], Nq, Nk, n_seq, _ptr(cu_q), _ptr(cu_k), int(bool(causal)), scale)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    return _lib.ParkAttnShape(B, D, _DT[q.dtype], Nq, k.shape[2], n_seq, _ptr(cu_q), _ptr(cu_k), bool(causal), scale)
 
 
-def _attn_check(Q, K, V):
-    _check("Q", Q)
-    if K.dim() != 4 or V.dim() != 4:
-        raise ValueError("K, V: expected CUDA tensors [B, H, N, D]")
-    B, H, _, D = Q.shape
-    _check("K", K, (B, K.shape[1], K.shape[2], D), Q.dtype, Q.device)
-    _check("V", V, K.shape, Q.dtype, Q.device)
-    if min(B, H, K.shape[1]) < 1 or H % K.shape[1]:
-        raise ValueError(f"{K.shape[1]} key heads do not divide {H} query heads")
+def _attn_check(Q, K, V) -> int:
+    if (not all(isinstance(t, torch.Tensor) for t in (Q, K, V)) or not _same(Q, K, V) or K.shape != V.shape
+            or K.shape[0] != Q.shape[0] or K.shape[3] != Q.shape[3]):
+        _check("Q", Q)
+        _check("K", K, None, Q.dtype, Q.device)
+        _check("K", K, (Q.shape[0], K.shape[1], K.shape[2], Q.shape[3]))
+        _check("V", V, K.shape, Q.dtype, Q.device)
+    B, H, hk = Q.shape[0], Q.shape[1], K.shape[1]
+    if B < 1 or H < 1 or hk < 1 or H % hk:
+        raise ValueError(f"{hk} key heads do not divide {H} query heads (batch {B})")
+    return Q.get_device()
 
 
 def _lse(lse, Q):
-    want = tuple(Q.shape[:3])
-    if tuple(lse.shape) != want or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != Q.device:
-        raise ValueError(f"lse must be contiguous float32 {want} on {Q.device}")
+    if lse.shape != Q.shape[:3] or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != Q.device:
+        raise ValueError(f"lse must be contiguous float32 {tuple(Q.shape[:3])} on {Q.device}")
     return lse
 
 
-def attention_workspace_size(Q, K, causal: bool = False, cu_q=None, cu_k=None, backward: bool = False) -> int:
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int, dtype: int, n_seq: int, backward: int) -> int:
+    # the bounds' addresses only have to be there
+    s, n = _lib.ParkAttnShape(B, D, dtype, Nq, Nk, n_seq, 1, 1, 0, 1.0), ctypes.c_size_t(0)
+    _lib.check(_lib.load().park_attention_workspace(ctypes.byref(s), Hq, Hk, backward, ctypes.byref(n)),
+               "park_attention_workspace")
+    return n.value
+
+
+def _attn_need(Q, K, s, backward: int) -> int:
+    return _attn_workspace(s.B, Q.shape[1], K.shape[1], s.Nq, s.Nk, s.D, s.dtype, s.n_seq, backward)
+
+
+def attention_workspace_size(Q, K, cu_q=None, cu_k=None, backward: bool = False) -> int:
     """Bytes of device workspace that attention (or attention_bwd) takes for these tensors."""
-    s, n = _attn_shape(Q, K, causal, None, cu_q, cu_k), ctypes.c_size_t(0)
-    _lib.check(_lib.load().park_attention_workspace(ctypes.byref(s), Q.shape[1], K.shape[1], int(backward),
-                                                    ctypes.byref(n)), "park_attention_workspace")
-    return int(n.value)
+    return _attn_need(Q, K, _attn_shape(Q, K, False, None, cu_q, cu_k), int(backward))
 
 
 def attention(Q, K, V, causal: bool = False, scale: float | None = None, cu_q=None, cu_k=None, O=None,
@@ -344,23 +416,20 @@ def attention(Q, K, V, causal: bool = False, scale: float | None = None, cu_q=No
     h // (Hq // Hk)).  cu_q, cu_k (int32 [n_seq + 1] on the device, B = 1) pack sequences
     of different, possibly zero, lengths; rows outside them are not written (in a new O
     they are undefined).  causal: row i sees keys j <= i + n_k - n_q.  Rows without a key
-    give 0 and lse = -inf.  scale defaults to 1/sqrt(D)."""
-    _attn_check(Q, K, V)
-    lib = _lib.load()
-    with _On(Q.device, stream) as st:
-        O = torch.empty_like(Q) if O is None else O
-        _check("O", O, Q.shape, Q.dtype, Q.device, output=True)
-        if lse is None:
-            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if return_lse else None
-        else:
+    give 0 and lse = -inf.  scale > 0 defaults to 1/sqrt(D)."""
+    index = _attn_check(Q, K, V)
+    with _On(index, stream) as st:
+        O = torch.empty_like(Q) if O is None else _output("O", O, Q)
+        if lse is not None:
             _lse(lse, Q)
-        s, need = _attn_shape(Q, K, causal, scale, cu_q, cu_k), ctypes.c_size_t(0)
-        _lib.check(lib.park_attention_workspace(ctypes.byref(s), Q.shape[1], K.shape[1], 0, ctypes.byref(need)),
-                   "park_attention_workspace")
-        ws = _workspace(ws, need.value, Q.device)
-        rc = lib.park_attention(ctypes.byref(s), _op(Q), _op(K), _op(V), _op(O), _ptr(lse), _ptr(ws),
-                                ws.numel() * ws.element_size(), _ptr(_status(status, Q.device)), st)
-    _lib.check(rc, "park_attention")
+        elif return_lse:
+            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+        s = _attn_shape(Q, K, causal, scale, cu_q, cu_k)
+        ws, wp, wn = _workspace(ws, _attn_need(Q, K, s, 0), Q)
+        rc = _lib.load().park_attention(s, _op("Q", Q), _op("K", K), _op("V", V), _op("O", O), _ptr(lse), wp, wn,
+                                        _status(status, index), st)
+    if rc:
+        _done(rc, "park_attention", (("Q", Q), ("K", K), ("V", V)), (("O", O),))
     return (O, lse) if return_lse else O
 
 
@@ -369,23 +438,20 @@ def attention_bwd(dO, Q, K, V, O, lse, causal: bool = False, scale: float | None
     """(dQ, dK, dV) from dO and from attention's inputs and results; dK and dV are sums
     over the query heads that share a key head.  Rows outside the packed sequences are
     not written (in new tensors they are undefined)."""
-    _attn_check(Q, K, V)
-    _check("O", O, Q.shape, Q.dtype, Q.device)
-    _check("dO", dO, Q.shape, Q.dtype, Q.device)
+    index = _attn_check(Q, K, V)
+    for name, t in (("O", O), ("dO", dO)):
+        if not isinstance(t, torch.Tensor) or not _same(Q, t) or t.shape != Q.shape:
+            _check(name, t, Q.shape, Q.dtype, Q.device)
     _lse(lse, Q)
-    lib = _lib.load()
-    with _On(Q.device, stream) as st:
-        outs = []
-        for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V)):
-            t = torch.empty_like(like) if t is None else t
-            _check(name, t, like.shape, Q.dtype, Q.device, output=True)
-            outs.append(t)
-        s, need = _attn_shape(Q, K, causal, scale, cu_q, cu_k), ctypes.c_size_t(0)
-        _lib.check(lib.park_attention_workspace(ctypes.byref(s), Q.shape[1], K.shape[1], 1, ctypes.byref(need)),
-                   "park_attention_workspace")
-        ws = _workspace(ws, need.value, Q.device)
-        rc = lib.park_attention_bwd(ctypes.byref(s), _op(dO), _op(Q), _op(K), _op(V), _op(O), _ptr(lse), _op(outs[0]),
-                                    _op(outs[1]), _op(outs[2]), _ptr(ws), ws.numel() * ws.element_size(),
-                                    _ptr(_status(status, Q.device)), st)
-    _lib.check(rc, "park_attention_bwd")
+    with _On(index, stream) as st:
+        outs = [torch.empty_like(like) if t is None else _output(name, t, like)
+                for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V))]
+        s = _attn_shape(Q, K, causal, scale, cu_q, cu_k)
+        ws, wp, wn = _workspace(ws, _attn_need(Q, K, s, 1), Q)
+        rc = _lib.load().park_attention_bwd(s, _op("dO", dO), _op("Q", Q), _op("K", K), _op("V", V), _op("O", O),
+                                            _ptr(lse), _op("dQ", outs[0]), _op("dK", outs[1]), _op("dV", outs[2]), wp,
+                                            wn, _status(status, index), st)
+    if rc:
+        _done(rc, "park_attention_bwd", (("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O)),
+              tuple(zip(("dQ", "dK", "dV"), outs)))
     return tuple(outs)
