@@ -45,21 +45,43 @@ struct BwdCfg {
 };
 
 struct DqSmem {
-    uint64_t own_full, kv_full[8], kv_empty[8], s_full, p_full, dp_full, ds_full, final_bar;
+    uint64_t own_full, kv_full[8], kv_empty[8], s_full, p_full[2], dp_full, ds_full, final_bar;
     uint32_t tmem_base;
     int abort;
     SeqTile seq;
     float sum[2][2][kTile];  // [column half][exact, of the rounded ds][row]
 };
 struct DkvSmem {
-    uint64_t own_full, in_full[8], in_empty[8], s_full, p_full, dp_full, ds_full, stat_full[2], stat_empty[2], final_bar;
+    uint64_t own_full, in_full[8], in_empty[8], s_full, p_full[2], dp_full, ds_full, stat_full[2], stat_empty[2], final_bar;
     uint32_t tmem_base;
     int abort, poison;
     SeqTile seq;
-    alignas(16) float lse2[2][kTile], delta[2][kTile];
+    alignas(16) float lse2[2][kTile], delta[2][kTile];  // both negated
 };
 template <int NP, typename S>
 constexpr size_t bwd_smem() { return (size_t)(2 + BwdCfg<NP>::ST) * BwdCfg<NP>::tile + sizeof(S); }
+
+// Pair e of exponentials.  At 128 columns the four products take longer than the exponentials and all of them go to
+// the special-function unit (moving two of eight pairs to the FMA pipe: dq 1.43 -> 1.51 ms at 16,384 x 8 heads); at
+// 64 columns the products are half as long and two of eight pairs go to the FMA pipe (dk/dv 0.56 -> 0.51 ms at
+// 8,192 causal, 16/4 heads).
+template <int NP>
+__device__ __forceinline__ float2 ex2_pair(int e, float2 x) {
+    return NP == 1 && e % 4 == 0 ? ex2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
+}
+// K = 16 steps of a product over 128 rows of which the threads deliver their first 32 columns, then the others
+__device__ constexpr int part_step(int part, int x) { return 2 * part + (x & 1) + 4 * (x >> 1); }
+
+// Pairs of columns c0 + 2e, c0 + 2e + 1: 0 outside lo .. hi.  (A hidden row's lse and delta may be NaN, so p and ds
+// are hidden once they are formed.)
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&pk)[N], int c0, int lo, int hi) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int c = c0 + 2 * e;
+        pk[e] &= (c >= lo && c <= hi ? 0x0000FFFFu : 0u) | (c + 1 >= lo && c + 1 <= hi ? 0xFFFF0000u : 0u);
+    }
+}
 
 // 64 columns at `col` of this thread's lane
 __device__ __forceinline__ void ld64(uint32_t col, uint32_t (&x)[2][32]) {
@@ -94,7 +116,8 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_init(&sh.kv_empty[s], 1);
             }
             mbar_init(&sh.s_full, 1);
-            mbar_init(&sh.p_full, 256);
+            mbar_init(&sh.p_full[0], 256);
+            mbar_init(&sh.p_full[1], 256);
             mbar_init(&sh.dp_full, 1);
             mbar_init(&sh.ds_full, 256);
             mbar_init(&sh.final_bar, 1);
@@ -166,18 +189,25 @@ __global__ void __launch_bounds__(384, 1)
             };
             // w = 0: B += P K; w = 1: dQ += dS K
             auto issue_g = [&](int j, int w) -> bool {
-                if (!wait_warp(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
-                tc_fence_after();
                 const int st = (2 * j) % C::ST;
                 const uint64_t ka = dBt + ((st * C::tile) >> 4);
-                if (lead) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
-                                     ka + ((kk * 2048) >> 4), idQ, j > 0 || kk > 0);
-                    if (w) umma_commit(&sh.kv_empty[st]);
+                for (int part = 0; part < 2; ++part) {
+                    if ((w == 0 || part == 0) &&
+                        !wait_warp(w ? &sh.ds_full : &sh.p_full[part], j & 1, abort, wait_ns))
+                        return false;
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int kk = part_step(part, x);
+                            umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
+                                         ka + ((kk * 2048) >> 4), idQ, j > 0 || part > 0 || x > 0);
+                        }
+                        if (part == 1 && w) umma_commit(&sh.kv_empty[st]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 return true;
             };
             bool ok = nt > 0 && wait_warp(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
@@ -212,26 +242,18 @@ __global__ void __launch_bounds__(384, 1)
                 break;
             }
             tc_fence_after();
-            uint32_t s[2][32], pk[32];
+            uint32_t s[2][32];
             ld64(trow + 64 * hc, s);
             tmem_ld_wait();
             tmem_ld_dep(s[0]);
             tmem_ld_dep(s[1]);
-            const int lim = j >= cut ? seen - j * kTile - 64 * hc : 64;  // columns 0 .. lim of this half are visible
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 x = __ffma2_rn(make_float2(f_of(s[c][2 * e]), f_of(s[c][2 * e + 1])), sl22, nl);
-                    const float p0 = ex2(x.x), p1 = ex2(x.y);
-                    s[c][2 * e] = __float_as_uint(p0);
-                    s[c][2 * e + 1] = __float_as_uint(p1);
-                    pk[16 * c + e] = bf2(p0, p1);
-                }
+            const int lim = seen - j * kTile - 64 * hc;  // columns 0 .. lim of this half are visible
             if (j >= cut) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    pk[e] &= (2 * e <= lim ? 0x0000FFFFu : 0u) | (2 * e + 1 <= lim ? 0xFFFF0000u : 0u);
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > lim) s[c][e] = 0xff800000u;  // p = 0
                 // K_j, which S has been formed from, is cleaned for the sums over its rows
                 const int st = (2 * j) % C::ST;
                 if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_full[st], ((2 * j) / C::ST) & 1, abort, wait_ns))) {
@@ -242,29 +264,42 @@ __global__ void __launch_bounds__(384, 1)
                 for (int e = threadIdx.x; e < (int)(C::tile / 16); e += 256) clean16(k4 + e);
                 fence_proxy_async_smem();
             }
-            tmem_st32(trow + 64 * hc, pk);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sh.p_full);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 p = ex2_pair<NP>(e, __ffma2_rn(make_float2(f_of(s[c][2 * e]), f_of(s[c][2 * e + 1])), sl22, nl));
+                    s[c][2 * e] = __float_as_uint(p.x);
+                    s[c][2 * e + 1] = __float_as_uint(p.y);
+                    pk[e] = bf2(p.x, p.y);
+                }
+                tmem_st16(trow + 64 * hc + 16 * c, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[c]);
+            }
             if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t g[32];
                 tmem_ld32(trow + 128 + 64 * hc + 32 * c, g);
                 tmem_ld_wait();
                 tmem_ld_dep(g);
+                if (j >= cut) {  // what a hidden value makes of dP does not meet p = 0
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > lim) g[e] = 0u;
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float2 x = __fmul2_rn(__fadd2_rn(make_float2(f_of(g[2 * e]), f_of(g[2 * e + 1])), nd),
-                                          make_float2(f_of(s[c][2 * e]), f_of(s[c][2 * e + 1])));
-                    if (j >= cut) {
-                        x.x = 32 * c + 2 * e <= lim ? x.x : 0.f;
-                        x.y = 32 * c + 2 * e + 1 <= lim ? x.y : 0.f;
-                    }
+                    const float2 x = __fmul2_rn(__fadd2_rn(make_float2(f_of(g[2 * e]), f_of(g[2 * e + 1])), nd),
+                                                make_float2(f_of(s[c][2 * e]), f_of(s[c][2 * e + 1])));
                     const uint32_t w = bf2(x.x, x.y);
                     r2 = __fadd2_rn(r2, x);
                     rb2 = __fadd2_rn(rb2, make_float2(f_of(w << 16), f_of(w & 0xFFFF0000u)));
@@ -351,7 +386,8 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_init(&sh.in_empty[s], 1);
             }
             mbar_init(&sh.s_full, 1);
-            mbar_init(&sh.p_full, 256);
+            mbar_init(&sh.p_full[0], 256);
+            mbar_init(&sh.p_full[1], 256);
             mbar_init(&sh.dp_full, 1);
             mbar_init(&sh.ds_full, 256);
             for (int s = 0; s < 2; ++s) {
@@ -431,18 +467,25 @@ __global__ void __launch_bounds__(384, 1)
             };
             // w = 0: dV += P^T dO; w = 1: dK += dS^T Q
             auto issue_g = [&](int j, int w) -> bool {
-                if (!wait_warp(w ? &sh.ds_full : &sh.p_full, j & 1, abort, wait_ns)) return false;
-                tc_fence_after();
                 const int st = (2 * j + 1 - w) % C::ST;
                 const uint64_t ba = dBt + ((st * C::tile) >> 4);
-                if (lead) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
-                                     ba + ((kk * 2048) >> 4), idG, j > 0 || kk > 0);
-                    umma_commit(&sh.in_empty[st]);
+                for (int part = 0; part < 2; ++part) {
+                    if ((w == 0 || part == 0) &&
+                        !wait_warp(w ? &sh.ds_full : &sh.p_full[part], j & 1, abort, wait_ns))
+                        return false;
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int kk = part_step(part, x);
+                            umma_bf16_ts(tm + 256 + 128 * w, tm + 128 * w + 64 * (kk >> 2) + 8 * (kk & 3),
+                                         ba + ((kk * 2048) >> 4), idG, j > 0 || part > 0 || x > 0);
+                        }
+                        if (part == 1) umma_commit(&sh.in_empty[st]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 return true;
             };
             bool ok = steps > 0 && wait_warp(&sh.own_full, 0, abort, wait_ns) && issue_s(0, 0) && issue_s(0, 1);
@@ -465,10 +508,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = lane + 32 * e, i = it * kTile + c;
-                    float l = i < t.nq ? a.lse[at + i] * kLog2e : INF;
-                    if (l == -INF) l = INF;  // a row without keys
+                    float l = i < t.nq ? a.lse[at + i] * -kLog2e : -INF;
+                    if (l == INF) l = -INF;  // a row without keys
                     sh.lse2[st][c] = l;
-                    sh.delta[st][c] = i < t.nq ? delta[at + i] : 0.f;
+                    sh.delta[st][c] = i < t.nq ? -delta[at + i] : 0.f;
                 }
                 mbar_arrive(&sh.stat_full[st]);
                 if (++it == end) {
@@ -498,34 +541,12 @@ __global__ void __launch_bounds__(384, 1)
             // columns lo .. hi of this half are visible to this thread's key
             const bool cut = i0 + kTile > t.nq || j0 + kTile - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
             const int lo = (a.causal ? j0 + row - off - i0 : 0) - 64 * hc, hi = t.nq - 1 - i0 - 64 * hc;
-            uint32_t s[2][32], pk[32];
+            uint32_t s[2][32];
             ld64(trow + 64 * hc, s);
             tmem_ld_wait();
             tmem_ld_dep(s[0]);
             tmem_ld_dep(s[1]);
-            const float4* lp = reinterpret_cast<const float4*>(&sh.lse2[st][64 * hc]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 l = lp[8 * c + e];
-                    const float2 x = __ffma2_rn(make_float2(f_of(s[c][4 * e]), f_of(s[c][4 * e + 1])), sl22,
-                                                make_float2(-l.x, -l.y));
-                    const float2 y = __ffma2_rn(make_float2(f_of(s[c][4 * e + 2]), f_of(s[c][4 * e + 3])), sl22,
-                                                make_float2(-l.z, -l.w));
-                    const float p0 = ex2(x.x), p1 = ex2(x.y), p2 = ex2(y.x), p3 = ex2(y.y);
-                    s[c][4 * e] = __float_as_uint(p0);
-                    s[c][4 * e + 1] = __float_as_uint(p1);
-                    s[c][4 * e + 2] = __float_as_uint(p2);
-                    s[c][4 * e + 3] = __float_as_uint(p3);
-                    pk[16 * c + 2 * e] = bf2(p0, p1);
-                    pk[16 * c + 2 * e + 1] = bf2(p2, p3);
-                }
             if (cut) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    pk[e] &= (2 * e >= lo && 2 * e <= hi ? 0x0000FFFFu : 0u) |
-                             (2 * e + 1 >= lo && 2 * e + 1 <= hi ? 0xFFFF0000u : 0u);
                 // S and dP have been formed from Q and dO: now they are cleaned for the sums over their rows
                 const int sq = (2 * j) % C::ST, sg = (2 * j + 1) % C::ST;
                 if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns) &&
@@ -542,16 +563,37 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 fence_proxy_async_smem();
             }
-            tmem_st32(trow + 64 * hc, pk);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sh.p_full);
+            const float4* lp = reinterpret_cast<const float4*>(&sh.lse2[st][64 * hc]);  // negated
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 l = lp[8 * c + e];
+                    const float2 x = ex2_pair<NP>(2 * e, __ffma2_rn(make_float2(f_of(s[c][4 * e]), f_of(s[c][4 * e + 1])), sl22,
+                                                                make_float2(l.x, l.y)));
+                    const float2 y = ex2_pair<NP>(2 * e + 1, __ffma2_rn(make_float2(f_of(s[c][4 * e + 2]), f_of(s[c][4 * e + 3])),
+                                                                    sl22, make_float2(l.z, l.w)));
+                    s[c][4 * e] = __float_as_uint(x.x);
+                    s[c][4 * e + 1] = __float_as_uint(x.y);
+                    s[c][4 * e + 2] = __float_as_uint(y.x);
+                    s[c][4 * e + 3] = __float_as_uint(y.y);
+                    pk[2 * e] = bf2(x.x, x.y);
+                    pk[2 * e + 1] = bf2(y.x, y.y);
+                }
+                if (cut) hide(pk, 32 * c, lo, hi);
+                tmem_st16(trow + 64 * hc + 16 * c, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[c]);
+            }
             if (!__all_sync(0xffffffffu, wait_bar(&sh.dp_full, j & 1, abort, wait_ns))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float4* dp4 = reinterpret_cast<const float4*>(&sh.delta[st][64 * hc]);
+            const float4* dp4 = reinterpret_cast<const float4*>(&sh.delta[st][64 * hc]);  // negated
+            uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t g[32];
@@ -562,22 +604,17 @@ __global__ void __launch_bounds__(384, 1)
                 for (int e = 0; e < 8; ++e) {
                     const float4 d = dp4[8 * c + e];
                     const float2 x = __fmul2_rn(
-                        __fadd2_rn(make_float2(f_of(g[4 * e]), f_of(g[4 * e + 1])), make_float2(-d.x, -d.y)),
+                        __fadd2_rn(make_float2(f_of(g[4 * e]), f_of(g[4 * e + 1])), make_float2(d.x, d.y)),
                         make_float2(f_of(s[c][4 * e]), f_of(s[c][4 * e + 1])));
                     const float2 y = __fmul2_rn(
-                        __fadd2_rn(make_float2(f_of(g[4 * e + 2]), f_of(g[4 * e + 3])), make_float2(-d.z, -d.w)),
+                        __fadd2_rn(make_float2(f_of(g[4 * e + 2]), f_of(g[4 * e + 3])), make_float2(d.z, d.w)),
                         make_float2(f_of(s[c][4 * e + 2]), f_of(s[c][4 * e + 3])));
                     pk[16 * c + 2 * e] = bf2(x.x, x.y);
                     pk[16 * c + 2 * e + 1] = bf2(y.x, y.y);
                 }
             }
             mbar_arrive(&sh.stat_empty[st]);
-            if (cut) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    pk[e] &= (2 * e >= lo && 2 * e <= hi ? 0x0000FFFFu : 0u) |
-                             (2 * e + 1 >= lo && 2 * e + 1 <= hi ? 0xFFFF0000u : 0u);
-            }
+            if (cut) hide(pk, 0, lo, hi);
             tmem_st32(trow + 128 + 64 * hc, pk);
             tmem_st_wait();
             tc_fence_before();

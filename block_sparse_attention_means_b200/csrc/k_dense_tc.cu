@@ -53,10 +53,10 @@ struct FwdSmem {
     SeqTile seq;
 };
 
-#ifndef POLY
-#define POLY 2
-#endif
-__device__ constexpr bool poly_pair(int e) { return (e * POLY) % 8 < POLY; }
+// Pairs of exponentials that go to the FMA pipe (see ex2_poly2): two of eight.  All on the special-function unit, an
+// iteration's exponentials take as long as its products: 1233 / 810 TFLOP/s at 16,384 x 8 heads, D = 128 / 64; with one
+// pair in four moved 1248 / 814, with three in eight 1203 / 830.
+__device__ constexpr bool poly_pair(int e) { return e % 4 == 0; }
 
 // The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
 struct Piece {
@@ -338,8 +338,6 @@ __global__ void __launch_bounds__(384, 1)
                 for (int e = 0; e < 32; ++e) {
                     const int c = 2 * h + (e >> 4), y = 2 * (e & 15);
                     const float2 d = __ffma2_rn(make_float2(f_of(x[c][y]), f_of(x[c][y + 1])), sl22, nm);
-                    // some of the exponentials on the FMA pipe, the others on the special-function unit, which alone
-                    // would take as long as the two products
                     const float2 pe = poly_pair(e) ? ex2_poly2(d) : make_float2(ex2(d.x), ex2(d.y));
                     l2[e & 1] = __fadd2_rn(l2[e & 1], pe);
                     pk[e] = bf2(pe.x, pe.y);
