@@ -9,23 +9,28 @@
 //
 // Bound by memory: every element is read once and written once (the backward
 // pass reads x and dy and forms r again, which costs no traffic).  A warp owns one
-// token and walks its heads, so the token's cos and sin are looked up once and stay
-// in registers for all heads of Q and K; the table (one entry for each position of
-// an axis, not for each token) stays in L1/L2.  A head row lies on LPR = D/8 lanes
-// (16 for D = 96, four of them idle) with 8 elements, four whole pairs, on each, in
-// either pair order, so the rotation needs no exchange between lanes; the norm's
-// sums are log2(LPR) shuffles.  Four rows are in flight for each lane group before
-// the first is used.
+// token and walks a side's heads, so the token's cos and sin are looked up once and
+// stay in registers; the table (one entry for each position of an axis, not for
+// each token) stays in L1/L2.  A head row lies on LPR = D/8 lanes (16 for D = 96, four
+// of them idle) with 8 elements, four whole pairs, on each, in either pair order,
+// so the rotation needs no exchange between lanes; the norm's sums are log2(LPR)
+// shuffles.
 #include "kernels.h"
 
 namespace park {
 namespace {
 
-constexpr int kWarps = 8;    // warps of a block
-constexpr int kUnroll = 4;   // head rows in flight for each lane group
+// Measured at 24 + 24 heads x 119,056 tokens and 40 + 40 x 75,600, D = 128, bf16.  Forward: 8 blocks of 4 warps 6.23 and
+// 6.21 TB/s (6 blocks 5.30 and 5.38, 12 with two rows in flight 5.97 and 6.04).  Backward: 4 blocks 5.92 and 6.22 TB/s (3
+// blocks 5.31 and 5.68, 6 blocks 5.39 and 5.69: more warps at once write to more places at once).
+constexpr int kWarps = 4, kBlocks = 8;  // warps of a block, blocks of an SM
+constexpr int kUnroll = 4;              // head rows in flight for each lane group
+constexpr int kBwdWarps = 4, kBwdBlocks = 4, kBwdStages = 5;
 
-struct Quad {  // the four pairs of a lane
-    float a[4], b[4];
+// The four pairs of a lane, as packed float32 pairs (one instruction for two elements): a[i] = the first
+// elements of pairs 2i and 2i + 1, b[i] their second ones.
+struct Quad {
+    float2 a[2], b[2];
 };
 
 struct RopeDev {
@@ -47,11 +52,11 @@ struct Heads {
 template <typename T>
 struct Raw;
 template <>
-struct Raw<bf16_t> {
+struct alignas(16) Raw<bf16_t> {
     uint32_t v[4];
 };
 template <>
-struct Raw<float> {
+struct alignas(16) Raw<float> {
     uint32_t v[8];
 };
 
@@ -84,72 +89,84 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 template <bool HALF>
 __device__ __forceinline__ Quad unpack(const Raw<bf16_t>& r) {
     Quad q;
-    if (HALF) {
-        q.a[0] = lo_f(r.v[0]); q.a[1] = hi_f(r.v[0]); q.a[2] = lo_f(r.v[1]); q.a[3] = hi_f(r.v[1]);
-        q.b[0] = lo_f(r.v[2]); q.b[1] = hi_f(r.v[2]); q.b[2] = lo_f(r.v[3]); q.b[3] = hi_f(r.v[3]);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            q.a[e] = lo_f(r.v[e]);
-            q.b[e] = hi_f(r.v[e]);
+    for (int i = 0; i < 2; ++i) {
+        if (HALF) {
+            q.a[i] = make_float2(lo_f(r.v[i]), hi_f(r.v[i]));
+            q.b[i] = make_float2(lo_f(r.v[2 + i]), hi_f(r.v[2 + i]));
+        } else {
+            q.a[i] = make_float2(lo_f(r.v[2 * i]), lo_f(r.v[2 * i + 1]));
+            q.b[i] = make_float2(hi_f(r.v[2 * i]), hi_f(r.v[2 * i + 1]));
         }
     }
     return q;
 }
 template <bool HALF>
 __device__ __forceinline__ Quad unpack(const Raw<float>& r) {
+    const float* v = reinterpret_cast<const float*>(r.v);
     Quad q;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        q.a[e] = __uint_as_float(r.v[HALF ? e : 2 * e]);
-        q.b[e] = __uint_as_float(r.v[HALF ? 4 + e : 2 * e + 1]);
+    for (int i = 0; i < 2; ++i) {
+        q.a[i] = HALF ? make_float2(v[2 * i], v[2 * i + 1]) : make_float2(v[4 * i], v[4 * i + 2]);
+        q.b[i] = HALF ? make_float2(v[4 + 2 * i], v[5 + 2 * i]) : make_float2(v[4 * i + 1], v[4 * i + 3]);
     }
     return q;
 }
 template <bool HALF>
 __device__ __forceinline__ void store_quad(const Quad& q, uint8_t* row, int l, int D, bf16_t) {
     if (HALF) {
-        *reinterpret_cast<uint2*>(row + 8 * l) = make_uint2(pack2(q.a[0], q.a[1]), pack2(q.a[2], q.a[3]));
-        *reinterpret_cast<uint2*>(row + D + 8 * l) = make_uint2(pack2(q.b[0], q.b[1]), pack2(q.b[2], q.b[3]));
+        *reinterpret_cast<uint2*>(row + 8 * l) = make_uint2(pack2(q.a[0].x, q.a[0].y), pack2(q.a[1].x, q.a[1].y));
+        *reinterpret_cast<uint2*>(row + D + 8 * l) = make_uint2(pack2(q.b[0].x, q.b[0].y), pack2(q.b[1].x, q.b[1].y));
     } else {
-        *reinterpret_cast<uint4*>(row + 16 * l) = make_uint4(pack2(q.a[0], q.b[0]), pack2(q.a[1], q.b[1]),
-                                                             pack2(q.a[2], q.b[2]), pack2(q.a[3], q.b[3]));
+        *reinterpret_cast<uint4*>(row + 16 * l) = make_uint4(pack2(q.a[0].x, q.b[0].x), pack2(q.a[0].y, q.b[0].y),
+                                                             pack2(q.a[1].x, q.b[1].x), pack2(q.a[1].y, q.b[1].y));
     }
 }
 template <bool HALF>
 __device__ __forceinline__ void store_quad(const Quad& q, uint8_t* row, int l, int D, float) {
     if (HALF) {
-        *reinterpret_cast<float4*>(row + 16 * l) = make_float4(q.a[0], q.a[1], q.a[2], q.a[3]);
-        *reinterpret_cast<float4*>(row + 2 * D + 16 * l) = make_float4(q.b[0], q.b[1], q.b[2], q.b[3]);
+        *reinterpret_cast<float4*>(row + 16 * l) = make_float4(q.a[0].x, q.a[0].y, q.a[1].x, q.a[1].y);
+        *reinterpret_cast<float4*>(row + 2 * D + 16 * l) = make_float4(q.b[0].x, q.b[0].y, q.b[1].x, q.b[1].y);
     } else {
-        *reinterpret_cast<float4*>(row + 32 * l) = make_float4(q.a[0], q.b[0], q.a[1], q.b[1]);
-        *reinterpret_cast<float4*>(row + 32 * l + 16) = make_float4(q.a[2], q.b[2], q.a[3], q.b[3]);
+        *reinterpret_cast<float4*>(row + 32 * l) = make_float4(q.a[0].x, q.b[0].x, q.a[0].y, q.b[0].y);
+        *reinterpret_cast<float4*>(row + 32 * l + 16) = make_float4(q.a[1].x, q.b[1].x, q.a[1].y, q.b[1].y);
     }
 }
 
 // The lane's four weights of each half of its pairs, 1 without weights.
 template <bool HALF>
 __device__ __forceinline__ Quad load_weights(const void* w, int wdtype, int l, int D, bool active) {
-    Quad q;
+    float a[4], b[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int ia = HALF ? 4 * l + e : 8 * l + 2 * e, ib = HALF ? D / 2 + 4 * l + e : 8 * l + 2 * e + 1;
         if (!w || !active) {
-            q.a[e] = q.b[e] = 1.f;
+            a[e] = b[e] = 1.f;
         } else if (wdtype == PARK_F32) {
-            q.a[e] = static_cast<const float*>(w)[ia];
-            q.b[e] = static_cast<const float*>(w)[ib];
+            a[e] = static_cast<const float*>(w)[ia];
+            b[e] = static_cast<const float*>(w)[ib];
         } else {
-            q.a[e] = Elem<bf16_t>::to_float(static_cast<const bf16_t*>(w), ia);
-            q.b[e] = Elem<bf16_t>::to_float(static_cast<const bf16_t*>(w), ib);
+            a[e] = Elem<bf16_t>::to_float(static_cast<const bf16_t*>(w), ia);
+            b[e] = Elem<bf16_t>::to_float(static_cast<const bf16_t*>(w), ib);
         }
+    }
+    Quad q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        q.a[i] = make_float2(a[2 * i], a[2 * i + 1]);
+        q.b[i] = make_float2(b[2 * i], b[2 * i + 1]);
     }
     return q;
 }
 
+// cos, sin and -sin of the lane's pairs
+struct Turn {
+    float2 c[2], s[2], n[2];
+};
+
 // cos and sin of the lane's four pairs (4l .. 4l+3) for token (b, n)
-__device__ __forceinline__ void token_angles(const RopeDev& rp, int b, long long n, int l, bool active, float sign,
-                                             float (&c)[4], float (&s)[4], int32_t* status) {
+__device__ __forceinline__ void lookup_angles(const RopeDev& rp, int b, long long n, int l, bool active, float sign,
+                                              float (&c)[4], float (&s)[4], int32_t* status) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         c[e] = 1.f;
@@ -169,11 +186,12 @@ __device__ __forceinline__ void token_angles(const RopeDev& rp, int b, long long
         }
     } else {
         const long long plane = (long long)rp.e1 * rp.e2;
-        if (n >= plane * rp.e0) return;
-        t = (int)(n / plane);
-        const int r = (int)(n - t * plane);
-        y = r / rp.e2;
-        w = r - y * rp.e2;
+        const uint32_t n32 = (uint32_t)n, p32 = plane > n ? n32 + 1u : (uint32_t)plane;  // (n < 2^31)
+        t = (int)(n32 / p32);
+        if (t >= rp.e0) return;
+        const uint32_t r = n32 - t * p32;
+        y = (int)(r / (uint32_t)rp.e2);
+        w = (int)(r - y * (uint32_t)rp.e2);
     }
     if (!active) return;
     const float2* t1 = rp.table + (size_t)rp.e0 * rp.n0;
@@ -197,56 +215,108 @@ __device__ __forceinline__ void token_angles(const RopeDev& rp, int b, long long
     }
 }
 
+__device__ __forceinline__ Turn token_angles(const RopeDev& rp, int b, long long n, int l, bool active, float sign,
+                                             int32_t* status) {
+    float c[4], s[4];
+    lookup_angles(rp, b, n, l, active, sign, c, s, status);
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        t.c[i] = make_float2(c[2 * i], c[2 * i + 1]);
+        t.s[i] = make_float2(s[2 * i], s[2 * i + 1]);
+        t.n[i] = make_float2(-s[2 * i], -s[2 * i + 1]);
+    }
+    return t;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+template <int LPR>
+__device__ __forceinline__ float2 row_sum(float2 v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1)
+        v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    return v;
+}
 
-__device__ __forceinline__ Quad rotate(const Quad& q, const float (&c)[4], const float (&s)[4]) {
+__device__ __forceinline__ Quad rotate(const Quad& q, const Turn& t) {
     Quad r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        r.a[e] = q.a[e] * c[e] - q.b[e] * s[e];
-        r.b[e] = q.a[e] * s[e] + q.b[e] * c[e];
+    for (int i = 0; i < 2; ++i) {
+        r.a[i] = __ffma2_rn(q.b[i], t.n[i], __fmul2_rn(q.a[i], t.c[i]));
+        r.b[i] = __ffma2_rn(q.a[i], t.s[i], __fmul2_rn(q.b[i], t.c[i]));
     }
     return r;
 }
+// sum of x y over the lane's elements
+__device__ __forceinline__ float dot(const Quad& x, const Quad& y) {
+    float2 v = __fmul2_rn(x.a[0], y.a[0]);
+    v = __ffma2_rn(x.a[1], y.a[1], v);
+    v = __ffma2_rn(x.b[0], y.b[0], v);
+    v = __ffma2_rn(x.b[1], y.b[1], v);
+    return v.x + v.y;
+}
+__device__ __forceinline__ Quad mul(const Quad& x, const Quad& y) {
+    Quad r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r.a[i] = __fmul2_rn(x.a[i], y.a[i]);
+        r.b[i] = __fmul2_rn(x.b[i], y.b[i]);
+    }
+    return r;
+}
+__device__ __forceinline__ Quad mul(const Quad& x, float f) {
+    const float2 f2 = make_float2(f, f);
+    return mul(x, Quad{{f2, f2}, {f2, f2}});
+}
+__device__ __forceinline__ Quad fma(const Quad& x, const Quad& y, const Quad& z) {
+    Quad r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r.a[i] = __ffma2_rn(x.a[i], y.a[i], z.a[i]);
+        r.b[i] = __ffma2_rn(x.b[i], y.b[i], z.b[i]);
+    }
+    return r;
+}
+__device__ __forceinline__ Quad fma(const Quad& x, float f, const Quad& z) {
+    const float2 f2 = make_float2(f, f);
+    return fma(x, Quad{{f2, f2}, {f2, f2}}, z);
+}
 
-// Work items are (token, chunk of the concatenated heads of Q and K); the launch
-// cuts the heads into chunks only when the tokens alone would not fill the SMs.
+// A warp owns a token and a chunk of the heads of Q or of K: blockIdx.y < cq counts the chunks of Q, the others those of K
+// (one chunk each unless the tokens alone would not fill the SMs).
 template <typename T, bool HALF, bool NORM, int LPR>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_rope(Heads q, Heads k, RopeDev rp, int B, long long N, int D, float eps, int wdtype, float sign, int chunk,
+__global__ void __launch_bounds__(32 * kWarps, kBlocks)
+    k_rope(Heads q, Heads k, RopeDev rp, int B, long long N, int D, float eps, int wdtype, float sign, int chunk, int cq,
            int32_t* status) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long tok = (long long)blockIdx.x * kWarps + warp;
     if (tok >= B * N) return;
-    const int b = (int)(tok / N);
+    const int b = B == 1 ? 0 : (int)((uint32_t)tok / (uint32_t)N);  // (B N < 2^31)
     const long long n = tok - (long long)b * N;
+    const bool isk = (int)blockIdx.y >= cq;
+    const int h0 = ((int)blockIdx.y - (isk ? cq : 0)) * chunk, h1 = min(isk ? k.H : q.H, h0 + chunk);
+    const long long xh = isk ? k.xh : q.xh, yh = isk ? k.yh : q.yh;
+    const uint8_t* x = isk ? k.x + b * k.xb + n * k.xn : q.x + b * q.xb + n * q.xn;
+    uint8_t* y = isk ? k.y + b * k.yb + n * k.yn : q.y + b * q.yb + n * q.yn;
     const int l = lane % LPR, grp = lane / LPR;
     const bool active = 8 * l < D;
     constexpr int RPW = 32 / LPR;  // rows of a warp step
-    float c[4], s[4];
-    token_angles(rp, b, n, l, active, sign, c, s, status);
-    Quad wq, wk;
-    if (NORM) {
-        wq = load_weights<HALF>(q.w, wdtype, l, D, active);
-        wk = load_weights<HALF>(k.w, wdtype, l, D, active);
-    }
-    const int Ht = q.H + k.H;
-    const int h0 = blockIdx.y * chunk, h1 = min(Ht, h0 + chunk);
+    const Turn turn = token_angles(rp, b, n, l, active, sign, status);
+    Quad w;
+    if (NORM) w = load_weights<HALF>(isk ? k.w : q.w, wdtype, l, D, active);
     const float inv_d = 1.f / (float)D;
     for (int h = h0 + grp; h - grp < h1; h += RPW * kUnroll) {
         Raw<T> raw[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int hh = h + u * RPW;
-            const bool isk = hh >= q.H;
-            const uint8_t* row = isk ? k.x + b * k.xb + (hh - q.H) * k.xh + n * k.xn : q.x + b * q.xb + hh * q.xh + n * q.xn;
             if (hh < h1 && active) {
-                load_raw<HALF>(raw[u], row, l, D);
+                load_raw<HALF>(raw[u], x + hh * xh, l, D);
             } else {
 #pragma unroll
                 for (uint32_t& v : raw[u].v) v = 0u;
@@ -255,159 +325,191 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int hh = h + u * RPW;
-            const bool isk = hh >= q.H;
             Quad v = unpack<HALF>(raw[u]);
             if (NORM) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ss += v.a[e] * v.a[e] + v.b[e] * v.b[e];
-                const float r = rsqrtf(row_sum<LPR>(ss) * inv_d + eps);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v.a[e] *= r * (isk ? wk.a[e] : wq.a[e]);
-                    v.b[e] *= r * (isk ? wk.b[e] : wq.b[e]);
-                }
+                const float r = rsqrtf(row_sum<LPR>(dot(v, v)) * inv_d + eps);
+                v = mul(v, mul(w, r));
             }
-            if (hh < h1 && active) {
-                uint8_t* row = isk ? k.y + b * k.yb + (hh - q.H) * k.yh + n * k.yn
-                                   : q.y + b * q.yb + hh * q.yh + n * q.yn;
-                store_quad<HALF>(rotate(v, c, s), row, l, D, T{});
-            }
+            if (hh < h1 && active) store_quad<HALF>(rotate(v, turn), y + hh * yh, l, D, T{});
         }
     }
 }
 
-// Backward of the norm and rotation.  Blocks stride over the items; each warp keeps
-// its part of dw (both sides) in registers over all of its rows, the block adds the
-// warps' parts in order and writes one partial row, and k_dw_reduce adds the blocks'.
+// Asynchronous copy of the lane's part of a row into its own shared-memory slot.
+template <bool HALF>
+__device__ __forceinline__ void copy_raw(Raw<bf16_t>* dst, const uint8_t* row, int l, int D) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (HALF) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(row + 8 * l) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d + 8), "l"(row + D + 8 * l) : "memory");
+    } else {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(row + 16 * l) : "memory");
+    }
+}
+template <bool HALF>
+__device__ __forceinline__ void copy_raw(Raw<float>* dst, const uint8_t* row, int l, int D) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(row + (HALF ? 16 * l : 32 * l)) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16),
+                 "l"(row + (HALF ? 2 * D + 16 * l : 32 * l + 16))
+                 : "memory");
+}
+
+// Backward of the norm and rotation.  Blocks below `bq` stride over the items (token, chunk of heads) of Q, the others over
+// those of K; each warp keeps its part of dw in registers over all of its rows, the block adds the warps' parts in order
+// and writes one partial row, and k_dw_reduce adds the blocks'.  A row needs three times the forward pass's
+// arithmetic: with scalar arithmetic instruction issue was the bound (76 % busy), with packed pairs and loads into registers
+// latency was; so the loads run kBwdStages steps ahead through the lane's own slots in shared memory, across tokens.
 template <typename T, bool HALF, int LPR>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_norm_rope_bwd(Heads q, Heads k, RopeDev rp, int B, long long N, int D, float eps, int wdtype, int chunk,
-                    int n_chunks, float* __restrict__ part, int32_t* status) {
-    __shared__ float red[kWarps][2][128];
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdBlocks)
+    k_norm_rope_bwd(Heads q, Heads k, RopeDev rp, int B, long long N, int D, float eps, int wdtype, int chunk, int bq,
+                    float* __restrict__ part, int32_t* status) {
+    __shared__ Raw<T> ring[kBwdWarps][kBwdStages][2][32];
+    __shared__ float red[kBwdWarps][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, grp = lane / LPR;
     const bool active = 8 * l < D;
     constexpr int RPW = 32 / LPR;
-    constexpr int U = 2;  // rows in flight (x and dy each)
-    const Quad wq = load_weights<HALF>(q.w, wdtype, l, D, active), wk = load_weights<HALF>(k.w, wdtype, l, D, active);
-    Quad dwq, dwk;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dwq.a[e] = dwq.b[e] = dwk.a[e] = dwk.b[e] = 0.f;
-    const int Ht = q.H + k.H;
+    const bool isk = (int)blockIdx.x >= bq;
+    const int block = (int)blockIdx.x - (isk ? bq : 0), blocks = isk ? (int)gridDim.x - bq : bq;
+    const int H = isk ? k.H : q.H;
+    const long long xb = isk ? k.xb : q.xb, xh = isk ? k.xh : q.xh, xn = isk ? k.xn : q.xn;
+    const long long gb = isk ? k.db : q.db, gh = isk ? k.dh : q.dh, gn = isk ? k.dn : q.dn;
+    const long long yb = isk ? k.yb : q.yb, yh = isk ? k.yh : q.yh, yn = isk ? k.yn : q.yn;
+    const uint8_t *px = isk ? k.x : q.x, *pg = isk ? k.dy : q.dy;
+    uint8_t* py = isk ? k.y : q.y;
+    const Quad w = load_weights<HALF>(isk ? k.w : q.w, wdtype, l, D, active);
+    const float2 zero = make_float2(0.f, 0.f);
+    Quad dw{{zero, zero}, {zero, zero}};
     const float inv_d = 1.f / (float)D;
-    const long long items = (long long)B * N * n_chunks;
-    for (long long it = (long long)blockIdx.x * kWarps + warp; it < items; it += (long long)gridDim.x * kWarps) {
-        const long long tok = it / n_chunks;
-        const int ch = (int)(it - tok * n_chunks);
-        const int b = (int)(tok / N);
-        const long long n = tok - (long long)b * N;
-        float c[4], s[4];
-        token_angles(rp, b, n, l, active, -1.f, c, s, status);
-        const int h0 = ch * chunk, h1 = min(Ht, h0 + chunk);
-        for (int h = h0 + grp; h - grp < h1; h += RPW * U) {
-            Raw<T> rx[U], rd[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * RPW;
-                const bool isk = hh >= q.H;
-                if (hh < h1 && active) {
-                    load_raw<HALF>(rx[u], isk ? k.x + b * k.xb + (hh - q.H) * k.xh + n * k.xn
-                                              : q.x + b * q.xb + hh * q.xh + n * q.xn, l, D);
-                    load_raw<HALF>(rd[u], isk ? k.dy + b * k.db + (hh - q.H) * k.dh + n * k.dn
-                                              : q.dy + b * q.db + hh * q.dh + n * q.dn, l, D);
-                } else {
-#pragma unroll
-                    for (uint32_t& v : rx[u].v) v = 0u;
-#pragma unroll
-                    for (uint32_t& v : rd[u].v) v = 0u;
-                }
+    // (chunks are cut only for few tokens: the items' count fits 32 bits)
+    const uint32_t n_chunks = (uint32_t)((H + chunk - 1) / chunk), items = (uint32_t)(B * N) * n_chunks;
+    const uint32_t stride = (uint32_t)blocks * kBwdWarps, first = (uint32_t)block * kBwdWarps + warp;
+    // walks: of the loads (x, dy) and of the arithmetic and stores (y)
+    uint32_t it_in = first, it_at = first, n_at = 0;
+    int left_in = 0, left_at = 0, b_at = 0;  // heads of the chunk that are left, from this lane group's
+    const uint8_t *in_x = nullptr, *in_g = nullptr;
+    uint8_t* at_y = nullptr;
+    auto token = [&](uint32_t it, int& b, uint32_t& n, int& h0, int& left) {
+        const uint32_t tok = n_chunks == 1 ? it : it / n_chunks, ch = it - tok * n_chunks;
+        b = B == 1 ? 0 : (int)(tok / (uint32_t)N);
+        n = tok - (uint32_t)b * (uint32_t)N;
+        h0 = (int)ch * chunk;
+        left = min(chunk, H - h0) - grp;
+        h0 += grp;
+    };
+    auto enter_in = [&]() {
+        if (it_in >= items) return;
+        int b, h0;
+        uint32_t n;
+        token(it_in, b, n, h0, left_in);
+        in_x = px + b * xb + n * xn + h0 * xh;
+        in_g = pg + b * gb + n * gn + h0 * gh;
+    };
+    auto enter_at = [&]() {
+        if (it_at >= items) return;
+        int h0;
+        token(it_at, b_at, n_at, h0, left_at);
+        at_y = py + b_at * yb + n_at * yn + h0 * yh;
+    };
+    enter_in();
+    enter_at();
+    int slot_in = 0, slot = 0;
+    auto fetch = [&]() {
+        if (it_in < items) {
+            if (left_in > 0 && active) {
+                copy_raw<HALF>(&ring[warp][slot_in][0][lane], in_x, l, D);
+                copy_raw<HALF>(&ring[warp][slot_in][1][lane], in_g, l, D);
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * RPW;
-                const bool isk = hh >= q.H;
-                Quad x = unpack<HALF>(rx[u]);
-                const Quad g = rotate(unpack<HALF>(rd[u]), c, s);
-                float ss = 0.f, hx = 0.f;
-                Quad hg;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    hg.a[e] = g.a[e] * (isk ? wk.a[e] : wq.a[e]);
-                    hg.b[e] = g.b[e] * (isk ? wk.b[e] : wq.b[e]);
-                    ss += x.a[e] * x.a[e] + x.b[e] * x.b[e];
-                    hx += hg.a[e] * x.a[e] + hg.b[e] * x.b[e];
-                }
-                const float r = rsqrtf(row_sum<LPR>(ss) * inv_d + eps);
-                const float m = row_sum<LPR>(hx) * r * inv_d;  // mean(h xh)
-                Quad dx;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float xa = x.a[e] * r, xb = x.b[e] * r;
-                    dx.a[e] = r * (hg.a[e] - xa * m);
-                    dx.b[e] = r * (hg.b[e] - xb * m);
-                    // rows past the end hold zeros and add nothing
-                    if (isk) {
-                        dwk.a[e] += g.a[e] * xa;
-                        dwk.b[e] += g.b[e] * xb;
-                    } else {
-                        dwq.a[e] += g.a[e] * xa;
-                        dwq.b[e] += g.b[e] * xb;
-                    }
-                }
-                if (hh < h1 && active)
-                    store_quad<HALF>(dx, isk ? k.y + b * k.yb + (hh - q.H) * k.yh + n * k.yn
-                                             : q.y + b * q.yb + hh * q.yh + n * q.yn, l, D, T{});
+            left_in -= RPW;
+            in_x += RPW * xh;
+            in_g += RPW * gh;
+            if (left_in + grp <= 0) {
+                it_in = items - it_in > stride ? it_in + stride : items;
+                enter_in();
             }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        slot_in = slot_in + 1 == kBwdStages ? 0 : slot_in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kBwdStages - 1; ++i) fetch();
+    Turn turn;
+    uint32_t angles_of = 0xffffffffu;
+    while (it_at < items) {
+        fetch();
+        if (angles_of != it_at) {
+            turn = token_angles(rp, b_at, n_at, l, active, -1.f, status);
+            angles_of = it_at;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+        const bool on = left_at > 0 && active;
+        Raw<T> rx, rd;
+        if (on) {
+            rx = ring[warp][slot][0][lane];
+            rd = ring[warp][slot][1][lane];
+        } else {
+#pragma unroll
+            for (uint32_t& v : rx.v) v = 0u;
+#pragma unroll
+            for (uint32_t& v : rd.v) v = 0u;
+        }
+        slot = slot + 1 == kBwdStages ? 0 : slot + 1;
+        const Quad xx = unpack<HALF>(rx);
+        const Quad g = rotate(unpack<HALF>(rd), turn);
+        const Quad gx = mul(g, xx);
+        const float2 sums = row_sum<LPR>(make_float2(dot(xx, xx), dot(gx, w)));  // sum x^2, sum h x
+        const float r = rsqrtf(sums.x * inv_d + eps);
+        dw = fma(gx, r, dw);  // (rows past the end hold zeros)
+        // dx = r (g w - x r mean(h xh)), mean(h xh) = r sum(h x) / D
+        const Quad dx = fma(g, mul(w, r), mul(xx, -r * r * r * sums.y * inv_d));
+        if (on) store_quad<HALF>(dx, at_y, l, D, T{});
+        left_at -= RPW;
+        at_y += RPW * yh;
+        if (left_at + grp <= 0) {
+            it_at = items - it_at > stride ? it_at + stride : items;
+            enter_at();
         }
     }
     // the lane groups of a warp, then the warps of the block, in a fixed order
+    float da[4] = {dw.a[0].x, dw.a[0].y, dw.a[1].x, dw.a[1].y}, db[4] = {dw.b[0].x, dw.b[0].y, dw.b[1].x, dw.b[1].y};
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            dwq.a[e] += __shfl_xor_sync(0xffffffffu, dwq.a[e], o);
-            dwq.b[e] += __shfl_xor_sync(0xffffffffu, dwq.b[e], o);
-            dwk.a[e] += __shfl_xor_sync(0xffffffffu, dwk.a[e], o);
-            dwk.b[e] += __shfl_xor_sync(0xffffffffu, dwk.b[e], o);
+            da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
+            db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
         }
     if (grp == 0 && active) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int ia = HALF ? 4 * l + e : 8 * l + 2 * e, ib = HALF ? D / 2 + 4 * l + e : 8 * l + 2 * e + 1;
-            red[warp][0][ia] = dwq.a[e];
-            red[warp][0][ib] = dwq.b[e];
-            red[warp][1][ia] = dwk.a[e];
-            red[warp][1][ib] = dwk.b[e];
+            red[warp][HALF ? 4 * l + e : 8 * l + 2 * e] = da[e];
+            red[warp][HALF ? D / 2 + 4 * l + e : 8 * l + 2 * e + 1] = db[e];
         }
     }
     __syncthreads();
-    const int side = threadIdx.x >> 7, d = threadIdx.x & 127;
-    if (d < D) {
+    for (int d = threadIdx.x; d < D; d += 32 * kBwdWarps) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += red[w][side][d];
-        part[((size_t)blockIdx.x * 2 + side) * D + d] = v;
+        for (int i = 0; i < kBwdWarps; ++i) v += red[i][d];
+        part[(size_t)blockIdx.x * D + d] = v;
     }
 }
 
-// dw[side][d] = sum over the blocks' partial rows; one warp for each 32 columns of a
-// row group, eight row groups added in order.
-__global__ void __launch_bounds__(256) k_dw_reduce(const float* __restrict__ part, int blocks, int D, float* dwq,
-                                                   float* dwk) {
-    __shared__ float red[8][32];
-    const int side = blockIdx.y, d = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+// dw = sum over the partial rows of a side's blocks: 32 columns by 32 groups of rows, the groups added in order.
+__global__ void __launch_bounds__(1024) k_dw_reduce(const float* __restrict__ part, int bq, int blocks, int D, float* dwq,
+                                                    float* dwk) {
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
+    const int i0 = blockIdx.y ? bq : 0, i1 = blockIdx.y ? blocks : bq;
     float v = 0.f;
-    for (int i = g; i < blocks; i += 8) v += part[((size_t)i * 2 + side) * D + d];
-    red[g][threadIdx.x & 31] = v;
+#pragma unroll 8
+    for (int i = i0 + g; i < i1; i += 32) v += part[(size_t)i * D + d];
+    red[g][lane] = v;
     __syncthreads();
-    if (g == 0) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-        float* out = side ? dwk : dwq;
-        if (out) out[d] = t;
-    }
+    const float t = warp_sum(red[lane][g]);  // warp g: column g
+    float* out = blockIdx.y ? dwk : dwq;
+    if (out && lane == 0) out[blockIdx.x * 32 + g] = t;
 }
 
 __global__ void k_rope_table(float2* table, int extent, int n, double theta, double scale) {
@@ -457,11 +559,11 @@ Heads heads(const park_operand* x, const park_operand* y, const park_operand* dy
     return h;
 }
 
-// Head chunks of an item: whole tokens when those give every SM its 64 warps, else
-// as many chunks as fill them, at least one step of a warp each.
-int head_chunk(long long tokens, int Ht, int rpw, int num_sms) {
-    const long long want = (64ll * num_sms + tokens - 1) / tokens;
-    long long chunk = (Ht + want - 1) / want;
+// Heads of a chunk: all of a side when the tokens of both sides alone give every SM its 64 warps, else as few as
+// fill them, at least one step of a warp.
+int head_chunk(long long tokens, int H, int rpw, int num_sms) {
+    const long long want = (32ll * num_sms + tokens - 1) / tokens;
+    long long chunk = (H + want - 1) / want;
     chunk = (chunk + rpw - 1) / rpw * rpw;
     return (int)(chunk < rpw ? rpw : chunk);
 }
@@ -488,15 +590,16 @@ int launch_rope(const park_operand* q, const park_operand* k, const park_operand
     const int elt = dtype == PARK_BF16 ? 2 : 4;
     const Heads hq = heads(q, yq, nullptr, wq, elt), hk = heads(k, yk, nullptr, wk, elt);
     const RopeDev rp = rope_dev(rope, pos, pos_sb);
-    const int Ht = hq.H + hk.H, lpr = D == 32 ? 4 : (D == 64 ? 8 : 16);
-    const int chunk = head_chunk(B * N, Ht, 32 / lpr, num_sms);
-    const dim3 grid((unsigned)((B * N + kWarps - 1) / kWarps), (unsigned)((Ht + chunk - 1) / chunk));
+    const int lpr = D == 32 ? 4 : (D == 64 ? 8 : 16);
+    const int chunk = head_chunk(B * N, hq.H > hk.H ? hq.H : hk.H, 32 / lpr, num_sms);
+    const int cq = (hq.H + chunk - 1) / chunk, ck = (hk.H + chunk - 1) / chunk;
+    const dim3 grid((unsigned)((B * N + kWarps - 1) / kWarps), (unsigned)(cq + ck));
     const float sign = inverse ? -1.f : 1.f;
     if (grid.y > 65535u) return PARK_ERR_UNSUPPORTED;
     const bool half = rope && rope->half;
     ::park::prof_begin(st);
 #define GO(T, HALF, NORM, LPR) \
-    k_rope<T, HALF, NORM, LPR><<<grid, 32 * kWarps, 0, st>>>(hq, hk, rp, B, N, D, eps, wdtype, sign, chunk, status)
+    k_rope<T, HALF, NORM, LPR><<<grid, 32 * kWarps, 0, st>>>(hq, hk, rp, B, N, D, eps, wdtype, sign, chunk, cq, status)
 #define GO_L(T, HALF, NORM)                     \
     do {                                        \
         if (lpr == 4) GO(T, HALF, NORM, 4);     \
@@ -523,9 +626,9 @@ int launch_rope(const park_operand* q, const park_operand* k, const park_operand
 }
 
 int norm_rope_bwd_blocks(long long tokens) {
-    if (tokens == 0) return 1;  // (writes dw = 0)
-    const long long b = (tokens * 4 + kWarps - 1) / kWarps;  // (small calls: several chunks of heads for each token)
-    return (int)(b < 592 ? b : 592);                          // four blocks for each of 148 SMs
+    // two sides at least; small calls cut a token's heads into chunks, so they may take more blocks than tokens / warps
+    const long long b = 2 + (tokens * 8 + kBwdWarps - 1) / kBwdWarps, most = (long long)kBwdBlocks * 148;
+    return (int)(b < most ? b : most);
 }
 
 int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const park_operand* q,
@@ -536,14 +639,16 @@ int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const
     const int elt = dtype == PARK_BF16 ? 2 : 4;
     const Heads hq = heads(q, dq, dyq, wq, elt), hk = heads(k, dk, dyk, wk, elt);
     const RopeDev rp = rope_dev(rope, pos, pos_sb);
-    const int Ht = hq.H + hk.H, lpr = D == 32 ? 4 : (D == 64 ? 8 : 16);
-    const int chunk = N ? head_chunk(B * N, Ht, 32 / lpr, num_sms) : Ht, nch = (Ht + chunk - 1) / chunk;
+    const int lpr = D == 32 ? 4 : (D == 64 ? 8 : 16);
+    const int Hm = hq.H > hk.H ? hq.H : hk.H, chunk = N ? head_chunk(B * N, Hm, 32 / lpr, num_sms) : Hm;
     const int blocks = norm_rope_bwd_blocks(B * N);
+    int bq = (int)((long long)blocks * hq.H / (hq.H + hk.H));  // shares of the blocks as the sides' rows
+    bq = bq < 1 ? 1 : (bq > blocks - 1 ? blocks - 1 : bq);
     const bool half = rope && rope->half;
     ::park::prof_begin(st);
 #define GO(T, HALF, LPR)                                                                                             \
-    k_norm_rope_bwd<T, HALF, LPR><<<blocks, 32 * kWarps, 0, st>>>(hq, hk, rp, B, N, D, eps, wdtype, chunk, nch, part, \
-                                                                  status)
+    k_norm_rope_bwd<T, HALF, LPR><<<blocks, 32 * kBwdWarps, 0, st>>>(hq, hk, rp, B, N, D, eps, wdtype, chunk, bq, \
+                                                                     part, status)
 #define GO_L(T, HALF)                    \
     do {                                 \
         if (lpr == 4) GO(T, HALF, 4);    \
@@ -562,7 +667,7 @@ int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const
     PARK_TRY_LAUNCH("k_norm_rope_bwd", st);
     if (!dwq && !dwk) return PARK_OK;
     ::park::prof_begin(st);
-    k_dw_reduce<<<dim3(D / 32, 2), 256, 0, st>>>(part, blocks, D, dwq, dwk);
+    k_dw_reduce<<<dim3(D / 32, 2), 1024, 0, st>>>(part, bq, blocks, D, dwq, dwk);
     PARK_TRY_LAUNCH("k_dw_reduce", st);
     return PARK_OK;
 }

@@ -203,7 +203,7 @@ int launch_rope(const park_operand* q, const park_operand* k, const park_operand
                 const void* wq, const void* wk, int wdtype, float eps, bool norm, const park_rope_axes* rope,
                 const int32_t* pos, long long pos_sb, bool inverse, int B, long long N, int D, int dtype,
                 int32_t* status, int num_sms, cudaStream_t st);
-int norm_rope_bwd_blocks(long long tokens);  // rows of `part`: float [blocks][2][D]
+int norm_rope_bwd_blocks(long long tokens);  // rows of `part`: float [blocks][D]
 int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const park_operand* q,
                          const park_operand* k, const park_operand* dq, const park_operand* dk, const void* wq,
                          const void* wk, int wdtype, float eps, const park_rope_axes* rope, const int32_t* pos,

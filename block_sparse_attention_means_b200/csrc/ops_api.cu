@@ -195,7 +195,7 @@ int park_qk_norm_rope(const park_operand* q, const park_operand* k, const void* 
 int park_qk_norm_rope_bwd_workspace(int B, int64_t N, int D, size_t* bytes) {
     if (!bytes || B < 1 || N < 0) return PARK_ERR_INVALID_ARG;
     if (D < 1 || D % 32 != 0 || D > 128 || N >= kMaxRows || B * N >= kMaxRows) return PARK_ERR_UNSUPPORTED;
-    *bytes = (size_t)norm_rope_bwd_blocks(B * N) * 2 * D * 4;
+    *bytes = (size_t)norm_rope_bwd_blocks(B * N) * D * 4;
     return PARK_OK;
 }
 
