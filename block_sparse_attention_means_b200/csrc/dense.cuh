@@ -20,12 +20,20 @@ struct DenseArgs {
     int32_t* status;
 };
 
-// How the forward pass on the tensor cores cuts its work: row tiles of a key head, parts that the
-// keys are split into (1: none) and the key tiles of a part; workspace for the parts.
+// How the forward pass cuts its work: rows of a tile, row tiles of a key head, parts that the keys are split into (1:
+// none) and the key tiles of a part; workspace for the parts.
 struct DenseSplit {
+    int rows;
     long long tiles;
     int n, chunk;
     size_t lse_off, bytes;
+};
+// How the kernel of dk and dv cuts its work: key tiles, parts that the steps (row tiles of all heads of a group) are split
+// into (1: none), steps of a part; float32 workspace of the parts, dk after dv.
+struct DkvSplit {
+    long long tiles;
+    int n, chunk;
+    size_t dk_off, bytes;
 };
 constexpr int kDenseSMs = 148;  // SMs of a B200
 
@@ -97,6 +105,12 @@ __device__ inline SeqTile dense_resolve(const DenseArgs& a, int x, int rows, boo
         before += __shfl_sync(0xffffffffu, pre, 31);
     }
     return t;
+}
+
+// Row tiles (of `tile` rows) first .. end-1 of each head that see a key of the key tile starting at j0.
+__device__ __forceinline__ void dense_row_tiles(const SeqTile& t, int j0, int causal, int tile, int& first, int& end) {
+    first = causal ? max(0, j0 - (t.nk - t.nq)) / tile : 0;
+    end = max(first, (t.nq + tile - 1) / tile);
 }
 
 // Keys that row i of a sequence sees: 0 .. dense_last_key (may be negative).

@@ -36,11 +36,11 @@ __device__ __forceinline__ float4 load4<bf16_t>(const uint8_t* p, int i) {
                        __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// rows 0 .. n-1 of `src` (row stride in elements) into a [64][D + 4] tile, zeros below
-template <int D>
+// rows 0 .. n-1 of `src` (row stride in elements) into a [ROWS][D + 4] tile, zeros below
+template <int D, int ROWS>
 __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long long stride, int n) {
     constexpr int C = D / 4;
-    for (int i = threadIdx.x; i < TB * C; i += 256) {
+    for (int i = threadIdx.x; i < ROWS * C; i += 256) {
         const int r = i / C, c = i - r * C;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n) v = load4<float>(src + r * stride * 4, c);
@@ -48,56 +48,59 @@ __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long l
     }
 }
 
-// s[i][j] = A[4 ty + i] . B[tx + 16 j]
-template <int D>
-__device__ __forceinline__ void dot_tile(float (&s)[4][4], const float* A, const float* Bm, int ty, int tx) {
+// s[i][j] = A[R ty + i] . B[tx + 16 j], even and odd elements in the halves of packed sums
+template <int D, int R>
+__device__ __forceinline__ void dot_tile(float (&s)[R][4], const float* A, const float* Bm, int ty, int tx) {
+    float2 t[R][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+        for (int j = 0; j < 4; ++j) t[i][j] = make_float2(0.f, 0.f);
+#pragma unroll(R > 4 ? 1 : 2)
     for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (D + 4) + d);
+        float4 b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * (D + 4) + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i) {
+            const float4 a = *reinterpret_cast<const float4*>(A + (R * ty + i) * (D + 4) + d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                t[i][j] = __ffma2_rn(make_float2(a.x, a.y), make_float2(b[j].x, b[j].y), t[i][j]);
+                t[i][j] = __ffma2_rn(make_float2(a.z, a.w), make_float2(b[j].z, b[j].w), t[i][j]);
             }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = t[i][j].x + t[i][j].y;
 }
 
-// acc[i][c] += sum_k P[4 ty + i][k] B[k][col c], col c = 2 tx + 32 (c / 2) + c % 2.
-// With MASK only pairs that see(row, k) allows enter the sum.
-template <int D, bool MASK, typename F>
-__device__ __forceinline__ void accumulate(float (&acc)[4][D / 16], const float* P, const float* Bm, int ty, int tx,
+// acc[i][c] += sum_k P[R ty + i][k] B[k][cols 2 tx + 32 c, + 1].  With MASK only pairs that see(row, k) allows enter.
+template <int D, int R, bool MASK, typename F>
+__device__ __forceinline__ void accumulate(float2 (&acc)[R][D / 32], const float* P, const float* Bm, int ty, int tx,
                                            F see) {
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < TB; k += 4) {
-        float4 p[4];
+        float4 p[R];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * PP + k);
+        for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(P + (R * ty + i) * PP + k);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 4; ++kk) {
+            float2 b[D / 32];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const float2 b = *reinterpret_cast<const float2*>(Bm + (k + kk) * (D + 4) + 2 * tx + 32 * c);
+            for (int c = 0; c < D / 32; ++c)
+                b[c] = *reinterpret_cast<const float2*>(Bm + (k + kk) * (D + 4) + 2 * tx + 32 * c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float pv = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                    if (!MASK || see(4 * ty + i, k + kk)) {
-                        acc[i][2 * c] = fmaf(pv, b.x, acc[i][2 * c]);
-                        acc[i][2 * c + 1] = fmaf(pv, b.y, acc[i][2 * c + 1]);
-                    }
+            for (int i = 0; i < R; ++i) {
+                const float pv = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                if (!MASK || see(R * ty + i, k + kk)) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) acc[i][c] = __ffma2_rn(make_float2(pv, pv), b[c], acc[i][c]);
                 }
             }
+        }
     }
 }
 
@@ -106,60 +109,94 @@ __device__ __forceinline__ void store2(uint8_t* row, int col, float x, float y) 
 }
 
 template <typename T>
+__device__ __forceinline__ void store4(uint8_t* row, int i, float4 v) {
+    if (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(row + 16 * i) = v;
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(row + 8 * i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+}
+
+template <typename T>
 __device__ __forceinline__ uint8_t* row_ptr(const Op4& o, int b, int h, long long n) {
     return o.p + (b * o.sb + h * o.sh + n * o.sn) * (long long)sizeof(T);
 }
 
-__device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, int x, bool by_keys) {
+__device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, int x, int rows, bool by_keys, int rep) {
     __shared__ SeqTile sh;
     if (threadIdx.x < 32) {
-        const SeqTile t = dense_resolve(a, x, TB, by_keys, 1);
+        const SeqTile t = dense_resolve(a, x, rows, by_keys, rep);
         if (threadIdx.x == 0) sh = t;
     }
     __syncthreads();
     return sh;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
+// Forward: 16 R rows of a sequence (counted token by token, the heads that share a key head side by side) and a part of
+// its keys.  With several parts each writes its normalised o and its log2-sum, joined by k_dense_combine.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+    k_dense_fwd_simt(DenseArgs a, int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse) {
+    constexpr int BM = 16 * R;
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
-    float* Ks = Qs + TB * (D + 4);
+    float* Ks = Qs + BM * (D + 4);
     float* Vs = Ks + TB * (D + 4);
     float* Ps = Vs + TB * (D + 4);
-    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, false);  // causal: long rows first
-    const int i0 = t.tile * TB;
-    if (!t.live || i0 >= t.nq) return;
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
+    const int G = a.Hq / a.Hk;
+    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, BM, false, G);  // causal: long rows first
+    const int r0 = t.tile * BM;
+    if (!t.live || r0 >= t.nq * G) return;
+    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int rows = min(TB, t.nq - i0);
-    load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-    float acc[4][D / 16], m[4], l[4];
+    const int rows = min(BM, t.nq * G - r0);
+    {
+        constexpr int C = D / 4;
+        for (int i = tid; i < BM * C; i += 256) {
+            const int r = i / C, c = i - r * C;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int tok = (r0 + r) / G, h = hk * G + (r0 + r - tok * G);
+                v = load4<float>(row_ptr<float>(a.q, b, h, t.q0 + tok), c);
+            }
+            *reinterpret_cast<float4*>(Qs + r * (D + 4) + 4 * c) = v;
+        }
+    }
+    float2 acc[R][D / 32];
+    float m[R], l[R];
+    int last[R];  // last visible key of each row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
+        last[i] = dense_last_key(min(r0 + R * ty + i, t.nq * G - 1) / G, t.nq, t.nk, a.causal);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
     }
     const float sl2 = a.scale * kLog2e;
-    const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;  // keys that any row sees
-    for (int j0 = 0; j0 < kend; j0 += TB) {
+    const int least = dense_last_key(r0 / G, t.nq, t.nk, a.causal);  // of the first row
+    int j_lo = 0, kend = dense_last_key((r0 + rows - 1) / G, t.nq, t.nk, a.causal) + 1;  // keys that any row sees
+    if (n_split > 1) {
+        j_lo = sp * chunk * TB;
+        kend = min(kend, j_lo + chunk * TB);
+    }
+    for (int j0 = j_lo; j0 < kend; j0 += TB) {
         __syncthreads();
-        load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
+        load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
+        load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
         __syncthreads();
-        auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
-        const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
-        float s[4][4];
-        dot_tile<D>(s, Qs, Ks, ty, tx);
+        const bool cut = j0 + TB - 1 > least;
+        float s[R][4];
+        dot_tile<D, R>(s, Qs, Ks, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             float mx = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[i][j] *= sl2;
-                if (cut && !see(4 * ty + i, tx + 16 * j)) s[i][j] = -INFINITY;
+                if (cut && j0 + tx + 16 * j > last[i]) s[i][j] = -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll
@@ -172,34 +209,80 @@ __global__ void __launch_bounds__(256) k_dense_fwd_simt(DenseArgs a) {
             for (int j = 0; j < 4; ++j) {
                 const float p = exp2f(s[i][j] - ref);
                 sum += p;
-                Ps[(4 * ty + i) * PP + tx + 16 * j] = p;
+                Ps[(R * ty + i) * PP + tx + 16 * j] = p;
             }
             l[i] = l[i] * alpha + sum;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) acc[i][c] *= alpha;
+            for (int c = 0; c < D / 32; ++c) acc[i][c] = __fmul2_rn(acc[i][c], make_float2(alpha, alpha));
         }
-        __syncthreads();
+        __syncwarp();  // (a row's probabilities come from its own half-warp)
         if (cut)
-            accumulate<D, true>(acc, Ps, Vs, ty, tx, see);
+            accumulate<D, R, true>(acc, Ps, Vs, ty, tx, [&](int r, int c) { return j0 + c <= last[r - R * ty]; });
         else
-            accumulate<D, false>(acc, Ps, Vs, ty, tx, see);
+            accumulate<D, R, false>(acc, Ps, Vs, ty, tx, [](int, int) { return true; });
     }
+    const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+    for (int i = 0; i < R; ++i) {
+        const int r = r0 + R * ty + i;
         float sum = l[i];
 #pragma unroll
         for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (r >= rows) continue;
-        const float inv = m[i] == -INFINITY && !(sum != sum) ? 0.f : 1.f / sum;
-        uint8_t* row = row_ptr<float>(a.o, b, h, t.q0 + i0 + r);
+        if (R * ty + i >= rows) continue;
+        const int tok = r / G, h = hk * G + (r - tok * G);
+        const bool none = m[i] == -INFINITY && sum == 0.f;
+        const float inv = none ? 0.f : 1.f / sum, lse = none ? -INFINITY : m[i] + log2f(sum);
+        const size_t id = ((size_t)b * a.Hq + h) * a.Nq + t.q0 + tok;
+        uint8_t* row = n_split > 1 ? reinterpret_cast<uint8_t*>(part_o + (sp * rows_all + id) * D)
+                                   : row_ptr<float>(a.o, b, h, t.q0 + tok);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            store2(row, 2 * tx + 32 * c, inv == 0.f ? 0.f : acc[i][2 * c] * inv,
-                      inv == 0.f ? 0.f : acc[i][2 * c + 1] * inv);
-        if (a.lse && tx == 0)
-            a.lse[((size_t)b * a.Hq + h) * a.Nq + t.q0 + i0 + r] = (m[i] + log2f(sum)) * kLn2;
+            store2(row, 2 * tx + 32 * c, none ? 0.f : acc[i][c].x * inv, none ? 0.f : acc[i][c].y * inv);
+        if (tx == 0) {
+            if (n_split > 1)
+                part_lse[sp * rows_all + id] = lse;
+            else if (a.lse)
+                a.lse[id] = lse * kLn2;
+        }
     }
+}
+
+// Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum; one warp a row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_dense_combine(DenseArgs a, int n_split, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+    const int lane = threadIdx.x & 31, G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
+    const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (x >= a.Nq * G) return;
+    const SeqTile t = dense_resolve(a, x, 1, false, G);  // tiles of one row
+    if (!t.live) return;
+    const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
+    const int tok = t.tile / G, head = hk * G + (t.tile - tok * G);
+    const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
+    float M = -INFINITY;
+    for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
+    M = warp_max(M);
+    const bool none = M == -INFINITY;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < n_split; ++s) {
+        const float ls = part_lse[s * rows_all + id];
+        if (ls == -INFINITY) continue;  // (its part of o may not be written)
+        const float w = exp2f(ls - M);
+        sum += w;
+        if (4 * lane < a.D) {
+            const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+    }
+    const float inv = none ? 0.f : 1.f / sum;
+    if (4 * lane < a.D)
+        store4<T>(row_ptr<T>(a.o, b, head, t.q0 + tok), lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
 }
 
 // delta [B, Hq, Nq]: one warp a row
@@ -227,15 +310,16 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
     float* Ks = Gs + TB * (D + 4);
     float* Vs = Ks + TB * (D + 4);
     float* Ps = Vs + TB * (D + 4);
-    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, false);
+    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, TB, false, 1);
     const int i0 = t.tile * TB;
     if (!t.live || i0 >= t.nq) return;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(TB, t.nq - i0);
-    load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-    load_tile<D>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
-    float acc[4][D / 16], lse2[4], del[4];
+    load_tile<D, TB>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+    load_tile<D, TB>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
+    float2 acc[4][D / 32];
+    float lse2[4], del[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
@@ -243,20 +327,20 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
         lse2[i] = r < rows ? a.lse[at] * kLog2e : 0.f;
         del[i] = r < rows ? delta[at] : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
     }
     const float sl2 = a.scale * kLog2e;
     const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;
     for (int j0 = 0; j0 < kend; j0 += TB) {
         __syncthreads();
-        load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
+        load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
+        load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
         __syncthreads();
         auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
         const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
         float s[4][4], dp[4][4];
-        dot_tile<D>(s, Qs, Ks, ty, tx);
-        dot_tile<D>(dp, Gs, Vs, ty, tx);
+        dot_tile<D, 4>(s, Qs, Ks, ty, tx);
+        dot_tile<D, 4>(dp, Gs, Vs, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -267,9 +351,9 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
             }
         __syncthreads();
         if (cut)
-            accumulate<D, true>(acc, Ps, Ks, ty, tx, see);
+            accumulate<D, 4, true>(acc, Ps, Ks, ty, tx, see);
         else
-            accumulate<D, false>(acc, Ps, Ks, ty, tx, see);
+            accumulate<D, 4, false>(acc, Ps, Ks, ty, tx, see);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -278,12 +362,13 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
         uint8_t* row = row_ptr<float>(a.dq, b, h, t.q0 + i0 + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            store2(row, 2 * tx + 32 * c, acc[i][2 * c] * a.scale, acc[i][2 * c + 1] * a.scale);
+            store2(row, 2 * tx + 32 * c, acc[i][c].x * a.scale, acc[i][c].y * a.scale);
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float* __restrict__ delta) {
+__global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float* __restrict__ delta, int n_split,
+                                                        int chunk, float* __restrict__ part_dv, float* __restrict__ part_dk) {
     extern __shared__ __align__(16) float smem[];
     float* Ks = smem;
     float* Vs = Ks + TB * (D + 4);
@@ -291,28 +376,32 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
     float* Gs = Qs + TB * (D + 4);
     float* Ps = Gs + TB * (D + 4);
     float* Ds = Ps + TB * PP;
-    const SeqTile t = resolve_block(a, blockIdx.x, true);  // causal: the first keys have the most rows
+    const SeqTile t = resolve_block(a, blockIdx.x, TB, true, 1);  // causal: the first keys have the most rows
     const int j0 = t.tile * TB;
     if (!t.live || j0 >= t.nk) return;
-    const int hk = blockIdx.y, b = blockIdx.z, G = a.Hq / a.Hk;
+    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split, G = a.Hq / a.Hk;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    int first, end;
+    dense_row_tiles(t, j0, a.causal, TB, first, end);
+    const int per = end - first, s0 = n_split > 1 ? sp * chunk : 0;
+    const int s1 = n_split > 1 ? min(per * G, s0 + chunk) : per * G;
+    if (n_split > 1 && s0 >= s1) return;  // (no such part)
     const int keys = min(TB, t.nk - j0);
-    load_tile<D>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
-    load_tile<D>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
-    float dk[4][D / 16], dv[4][D / 16];
+    load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
+    load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
+    float2 dk[4][D / 32], dv[4][D / 32];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) dk[i][c] = dv[i][c] = make_float2(0.f, 0.f);
     const float sl2 = a.scale * kLog2e;
-    const int first = a.causal ? max(0, j0 - (t.nk - t.nq)) / TB * TB : 0;  // first row tile that sees a key here
-    for (int g = 0; g < G; ++g) {
-        const int h = hk * G + g;
-        for (int i0 = first; i0 < t.nq; i0 += TB) {
+    {
+        for (int step = s0; step < s1; ++step) {
+            const int h = hk * G + step / per, i0 = (first + step % per) * TB;
             const int rows = min(TB, t.nq - i0);
             __syncthreads();
-            load_tile<D>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-            load_tile<D>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
+            load_tile<D, TB>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+            load_tile<D, TB>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
             __syncthreads();
             // r: key of the tile, c: query row of the tile
             auto see = [&](int r, int c) {
@@ -320,8 +409,8 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
             };
             const bool cut = rows < TB || j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
             float s[4][4], dp[4][4];
-            dot_tile<D>(s, Ks, Qs, ty, tx);
-            dot_tile<D>(dp, Vs, Gs, ty, tx);
+            dot_tile<D, 4>(s, Ks, Qs, ty, tx);
+            dot_tile<D, 4>(dp, Vs, Gs, ty, tx);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = tx + 16 * j;
@@ -338,11 +427,11 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
             }
             __syncthreads();
             if (cut) {
-                accumulate<D, true>(dv, Ps, Gs, ty, tx, see);
-                accumulate<D, true>(dk, Ds, Qs, ty, tx, see);
+                accumulate<D, 4, true>(dv, Ps, Gs, ty, tx, see);
+                accumulate<D, 4, true>(dk, Ds, Qs, ty, tx, see);
             } else {
-                accumulate<D, false>(dv, Ps, Gs, ty, tx, see);
-                accumulate<D, false>(dk, Ds, Qs, ty, tx, see);
+                accumulate<D, 4, false>(dv, Ps, Gs, ty, tx, see);
+                accumulate<D, 4, false>(dk, Ds, Qs, ty, tx, see);
             }
         }
     }
@@ -350,29 +439,75 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= keys) continue;
-        uint8_t* rk = row_ptr<float>(a.dk, b, hk, t.k0 + j0 + r);
-        uint8_t* rv = row_ptr<float>(a.dv, b, hk, t.k0 + j0 + r);
+        uint8_t *rk, *rv;
+        if (n_split > 1) {
+            const size_t at = (((size_t)sp * a.B + b) * a.Hk + hk) * a.Nk + t.k0 + j0 + r;
+            rk = reinterpret_cast<uint8_t*>(part_dk + at * D);
+            rv = reinterpret_cast<uint8_t*>(part_dv + at * D);
+        } else {
+            rk = row_ptr<float>(a.dk, b, hk, t.k0 + j0 + r);
+            rv = row_ptr<float>(a.dv, b, hk, t.k0 + j0 + r);
+        }
+        const float f = n_split > 1 ? 1.f : a.scale;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            store2(rk, 2 * tx + 32 * c, dk[i][2 * c] * a.scale, dk[i][2 * c + 1] * a.scale);
-            store2(rv, 2 * tx + 32 * c, dv[i][2 * c], dv[i][2 * c + 1]);
+            store2(rk, 2 * tx + 32 * c, dk[i][c].x * f, dk[i][c].y * f);
+            store2(rv, 2 * tx + 32 * c, dv[i][c].x, dv[i][c].y);
         }
     }
 }
 
-template <int D>
-int fwd_simt(const DenseArgs& a, cudaStream_t st) {
-    const size_t sm = (size_t)(3 * TB * (D + 4) + TB * PP) * 4;
-    cudaFuncSetAttribute(k_dense_fwd_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-    const dim3 grid((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B);
+// dk, dv = sums of the parts, in order; one warp a key row
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_dense_dkv_reduce(DenseArgs a, int tile, int n_split, int chunk, const float* __restrict__ part_dv,
+                       const float* __restrict__ part_dk) {
+    const int lane = threadIdx.x & 31, hk = blockIdx.y, b = blockIdx.z;
+    const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (x >= a.Nk) return;
+    const SeqTile t = dense_resolve(a, x, 1, true, 1);  // tiles of one key
+    if (!t.live || 4 * lane >= a.D) return;
+    int first, end;
+    dense_row_tiles(t, t.tile / tile * tile, a.causal, tile, first, end);
+    const int n = min(n_split, ((end - first) * (a.Hq / a.Hk) + chunk - 1) / chunk);  // parts that were written
+    const size_t at = (((size_t)b * a.Hk + hk) * a.Nk + t.k0 + t.tile) * a.D + 4 * lane, step = (size_t)a.B * a.Hk * a.Nk * a.D;
+    for (int w = 0; w < 2; ++w) {
+        const float* src = (w ? part_dk : part_dv) + at;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float4 u = *reinterpret_cast<const float4*>(src + s * step);
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+        const float f = w ? a.scale : 1.f;
+        store4<T>(row_ptr<T>(w ? a.dk : a.dv, b, hk, t.k0 + t.tile), lane, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+    }
+}
+
+template <int D, int R>
+int fwd_simt_r(const DenseArgs& a, const DenseSplit& sp, float* part_o, float* part_lse, cudaStream_t st) {
+    const size_t sm = (size_t)((16 * R + 2 * TB) * (D + 4) + 16 * R * PP) * 4;
+    cudaFuncSetAttribute(k_dense_fwd_simt<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     ::park::prof_begin(st);
-    k_dense_fwd_simt<D><<<grid, 256, sm, st>>>(a);
+    k_dense_fwd_simt<D, R><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 256, sm, st>>>(a, sp.n, sp.chunk, part_o, part_lse);
     PARK_TRY_LAUNCH("k_dense_fwd_simt", st);
     return PARK_OK;
 }
 
 template <int D>
-int bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st) {
+int fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st) {
+    const DenseSplit sp = dense_split_simt(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
+    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    float* part_o = static_cast<float*>(ws);
+    float* part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sp.lse_off);
+    PARK_CHECK(sp.rows == 128 ? (fwd_simt_r<D, 8>(a, sp, part_o, part_lse, st))
+               : sp.rows == 64 ? (fwd_simt_r<D, 4>(a, sp, part_o, part_lse, st))
+                               : (fwd_simt_r<D, 1>(a, sp, part_o, part_lse, st)));
+    return sp.n > 1 ? launch_dense_combine(a, PARK_F32, sp.n, part_o, part_lse, st) : PARK_OK;
+}
+
+template <int D>
+int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t st) {
     const size_t sq = (size_t)(4 * TB * (D + 4) + TB * PP) * 4, sk = sq + (size_t)TB * PP * 4;
     cudaFuncSetAttribute(k_dense_dq_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
     cudaFuncSetAttribute(k_dense_dkv_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
@@ -382,13 +517,108 @@ int bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st) {
         PARK_TRY_LAUNCH("k_dense_dq_simt", st);
     }
     if (a.Nk == 0) return PARK_OK;
+    const DkvSplit sp = dense_split_dkv(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, D, TB);
+    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    float* part_dk = parts + sp.dk_off / 4;
     ::park::prof_begin(st);
-    k_dense_dkv_simt<D><<<dim3((unsigned)dense_tiles(a.Nk, a.n_seq, TB), a.Hk, a.B), 256, sk, st>>>(a, delta);
+    k_dense_dkv_simt<D><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 256, sk, st>>>(a, delta, sp.n, sp.chunk, parts, part_dk);
     PARK_TRY_LAUNCH("k_dense_dkv_simt", st);
-    return PARK_OK;
+    return sp.n > 1 ? launch_dense_dkv_reduce(a, PARK_F32, sp, TB, parts, part_dk, st) : PARK_OK;
 }
 
 }  // namespace
+
+int launch_dense_combine(const DenseArgs& a, int dtype, int n_split, const float* part_o, const float* part_lse,
+                         cudaStream_t st) {
+    const dim3 grid((unsigned)((a.Nq * (a.Hq / a.Hk) + 7) / 8), a.Hk, a.B);
+    ::park::prof_begin(st);
+    if (dtype == PARK_BF16)
+        k_dense_combine<bf16_t><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+    else
+        k_dense_combine<float><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+    PARK_TRY_LAUNCH("k_dense_combine", st);
+    return PARK_OK;
+}
+
+int launch_dense_dkv_reduce(const DenseArgs& a, int dtype, const DkvSplit& sp, int tile, const float* dv, const float* dk,
+                            cudaStream_t st) {
+    const dim3 grid((unsigned)((a.Nk + 7) / 8), a.Hk, a.B);
+    ::park::prof_begin(st);
+    if (dtype == PARK_BF16)
+        k_dense_dkv_reduce<bf16_t><<<grid, 256, 0, st>>>(a, tile, sp.n, sp.chunk, dv, dk);
+    else
+        k_dense_dkv_reduce<float><<<grid, 256, 0, st>>>(a, tile, sp.n, sp.chunk, dv, dk);
+    PARK_TRY_LAUNCH("k_dense_dkv_reduce", st);
+    return PARK_OK;
+}
+
+// Few keys under many rows (text keys): the key tiles alone leave SMs idle, so the rows are split, about two CTAs for each
+// SM, at least 8 steps each.
+DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D, int tile) {
+    DkvSplit s;
+    s.tiles = dense_tiles(Nk, n_seq, tile);
+    s.n = 1;
+    s.chunk = 0;
+    const long long G = Hq / Hk, steps = (Nq + tile - 1) / tile * G, ctas = s.tiles * Hk * B;
+    if (ctas * 2 <= kDenseSMs) {
+        const long long work = n_seq > 0 ? (steps + n_seq * G) * ((s.tiles + n_seq - 1) / n_seq) * Hk : steps * ctas;
+        long long chunk = (work + 2 * kDenseSMs - 1) / (2 * kDenseSMs);
+        if (chunk < 8) chunk = 8;
+        const long long n = (steps + chunk - 1) / chunk;  // (a sequence has at most all the steps)
+        if (n > 1) {
+            s.n = (int)n;
+            s.chunk = (int)chunk;
+        }
+    }
+    const size_t one = align_up((size_t)B * Hk * Nk * D * 4 * (size_t)s.n, 256);
+    s.dk_off = s.n > 1 ? one : 0;
+    s.bytes = s.n > 1 ? 2 * one : 0;
+    return s;
+}
+
+// Splits the keys when the row tiles alone leave SMs idle: parts of equal length whatever the sequence (a packed batch
+// holds at most kt key tiles in all, a batch entry has as many), about `waves` CTAs for each SM, at least `least` key
+// tiles each.
+static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long long kt, int n_seq, int D, int waves,
+                       int least) {
+    s->n = 1;
+    s->chunk = 0;
+    const long long work = n_seq > 0 ? kt * Hk : kt * Hk * B * s->tiles;
+    long long chunk = (work + (long long)waves * kDenseSMs - 1) / ((long long)waves * kDenseSMs);
+    if (chunk < least) chunk = least;
+    const long long n = (kt + chunk - 1) / chunk;
+    if (s->tiles * Hk * B * 2 <= kDenseSMs * (waves > 2 ? 2 : 1) && n > 1) {
+        s->n = (int)n;
+        s->chunk = (int)chunk;
+    }
+    const size_t rows = (size_t)B * Hq * Nq;
+    s->lse_off = s->n > 1 ? align_up((size_t)s->n * rows * D * 4, 256) : 0;
+    s->bytes = s->n > 1 ? s->lse_off + align_up((size_t)s->n * rows * 4, 256) : 0;
+}
+
+DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
+    DenseSplit s;
+    s.rows = 256;
+    s.tiles = dense_tiles(Nq * (Hq / Hk), n_seq, s.rows);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 4);
+    return s;
+}
+
+DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
+    // the widest row tile that still fills the SMs: 8 rows a thread need half the shared-memory reads of 4, and one row a
+    // thread suits single rows
+    DenseSplit s;
+    const long long rows = Nq * (Hq / Hk), mean = n_seq > 0 ? rows / n_seq : rows;
+    s.rows = 16;
+    for (int r : {128, 64})
+        if (mean >= r / 2 && dense_tiles(rows, n_seq, r) * Hk * B >= kDenseSMs) {
+            s.rows = r;
+            break;
+        }
+    s.tiles = dense_tiles(rows, n_seq, s.rows);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2);
+    return s;
+}
 
 int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st) {
     const long long rows = (long long)a.B * a.Hq * a.Nq;
@@ -406,10 +636,10 @@ int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t
     (a.D == 32 ? F<32>(__VA_ARGS__) : a.D == 64 ? F<64>(__VA_ARGS__) \
      : a.D == 96 ? F<96>(__VA_ARGS__) : F<128>(__VA_ARGS__))
 
-int launch_dense_fwd_simt(const DenseArgs& a, cudaStream_t st) { return PARK_BY_D(fwd_simt, a, st); }
+int launch_dense_fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st) { return PARK_BY_D(fwd_simt, a, ws, st); }
 
-int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st) {
-    return PARK_BY_D(bwd_simt, a, delta, st);
+int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t st) {
+    return PARK_BY_D(bwd_simt, a, delta, parts, st);
 }
 
 }  // namespace park

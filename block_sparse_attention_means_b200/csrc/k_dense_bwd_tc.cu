@@ -363,7 +363,8 @@ template <int NP>
 __global__ void __launch_bounds__(384, 1)
     k_dense_dkv_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
-                   const float* __restrict__ delta, uint64_t wait_ns) {
+                   const float* __restrict__ delta, int n_split, int chunk, float* __restrict__ part_dv,
+                   float* __restrict__ part_dk, uint64_t wait_ns) {
     using C = BwdCfg<NP>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* Ks = smem;
@@ -408,11 +409,14 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const SeqTile t = sh.seq;
-    const int hk = blockIdx.y, b = blockIdx.z, G = a.Hq / a.Hk;
+    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split, G = a.Hq / a.Hk;
     const int j0 = t.tile * kTile, keys = t.live ? min(kTile, t.nk - j0) : 0;
-    // row tiles first .. end-1 of each head of the group see a key of this tile
-    const int first = a.causal ? max(0, j0 - (t.nk - t.nq)) / kTile : 0, end = (t.nq + kTile - 1) / kTile;
-    const int per = keys > 0 ? max(0, end - first) : 0, steps = per * G;
+    // row tiles first .. end-1 of each head of the group see a key of this tile; this part has steps s0 .. s0 + steps - 1
+    int first, end;
+    dense_row_tiles(t, j0, a.causal, kTile, first, end);
+    const int per = keys > 0 ? end - first : 0, s0 = n_split > 1 ? sp * chunk : 0;
+    const int steps = max(0, n_split > 1 ? min(chunk, per * G - s0) : per * G);
+    const int head0 = hk * G + (per > 0 ? s0 / per : 0), it0 = first + (per > 0 ? s0 % per : 0);
 
     if (warp >= 8) {
         reg_dec<56>();
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(384, 1)
                 tma_load_4d(Ks + p * kPanel, &tmK, &sh.own_full, 64 * p, t.k0 + j0, hk, b);
                 tma_load_4d(Vs + p * kPanel, &tmV, &sh.own_full, 64 * p, t.k0 + j0, hk, b);
             }
-            int issued = 0, head = hk * G, it = first;
+            int issued = 0, head = head0, it = it0;
             for (int i = 0; i < 2 * steps; ++i) {  // Q_0 dO_0 Q_1 dO_1 ...
                 const int st = i % C::ST, round = i / C::ST;
                 if (round > 0 && !wait_bar(&sh.in_empty[st], (round - 1) & 1, abort, wait_ns)) break;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(384, 1)
         } else if (warp == 10) {
             // lse and delta of each step's 128 rows
             const float INF = __int_as_float(0x7f800000);
-            int head = hk * G, it = first;
+            int head = head0, it = it0;
             for (int j = 0; j < steps; ++j) {
                 const int st = j & 1, round = j >> 1;
                 if (round > 0 && !__all_sync(0xffffffffu, wait_bar(&sh.stat_empty[st], (round - 1) & 1, abort, wait_ns))) break;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(384, 1)
         const float2 sl22 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
         const int off = t.nk - t.nq;
         bool ok = true;
-        int it = first;
+        int it = it0;
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1, i0 = it * kTile;
             if (++it == end) it = first;
@@ -621,13 +625,15 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive(&sh.ds_full);
         }
         if (steps > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&sh.final_bar, 0, abort, wait_ns)) && !__any_sync(0xffffffffu, *abort != 0);
-        if (ok) {
+        if (ok && !(n_split > 1 && steps == 0)) {  // (a part without steps is not written)
             tc_fence_after();
-            const bool live = row < keys;
+            const bool live = row < keys, split = n_split > 1;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const Op4& out_op = w ? a.dk : a.dv;
                 uint8_t* out = out_op.p + (b * out_op.sb + hk * out_op.sh + (t.k0 + j0 + (long long)row) * out_op.sn) * 2;
+                float* part = (w ? part_dk : part_dv) +
+                              ((((size_t)sp * a.B + b) * a.Hk + hk) * a.Nk + t.k0 + j0 + row) * a.D;
                 const float f = w ? a.scale : 1.f;
 #pragma unroll
                 for (int c = 0; c < NP; ++c) {
@@ -657,7 +663,11 @@ __global__ void __launch_bounds__(384, 1)
                                         o[e] = __float_as_uint(f_of(o[e]) + f_of((uint32_t)gr[e] << 16));
                             }
                     }
-                    if (live) {
+                    if (live && split) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(part + d0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint32_t x4[4];
@@ -681,7 +691,7 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 template <int NP>
-int bwd_tc(const DenseArgs& a, const CUtensorMap* m, float* delta, cudaStream_t st) {
+int bwd_tc(const DenseArgs& a, const CUtensorMap* m, float* delta, float* parts, cudaStream_t st) {
     constexpr size_t sq = bwd_smem<NP, DqSmem>(), sk = bwd_smem<NP, DkvSmem>();
     cudaFuncSetAttribute(k_dense_dq_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
     cudaFuncSetAttribute(k_dense_dkv_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
@@ -692,17 +702,21 @@ int bwd_tc(const DenseArgs& a, const CUtensorMap* m, float* delta, cudaStream_t 
         PARK_TRY_LAUNCH("k_dense_dq_tc", st);
     }
     if (a.Nk > 0) {
+        const DkvSplit sp = dense_split_dkv(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D, kTile);
+        if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+        float* part_dk = parts + sp.dk_off / 4;
         ::park::prof_begin(st);
-        k_dense_dkv_tc<NP><<<dim3((unsigned)dense_tiles(a.Nk, a.n_seq, kTile), a.Hk, a.B), 384, sk, st>>>(
-            m[0], m[1], m[2], m[3], a, delta, wait_limit_ns());
+        k_dense_dkv_tc<NP><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 384, sk, st>>>(
+            m[0], m[1], m[2], m[3], a, delta, sp.n, sp.chunk, parts, part_dk, wait_limit_ns());
         PARK_TRY_LAUNCH("k_dense_dkv_tc", st);
+        if (sp.n > 1) return launch_dense_dkv_reduce(a, PARK_BF16, sp, kTile, parts, part_dk, st);
     }
     return PARK_OK;
 }
 
 }  // namespace
 
-int launch_dense_bwd_tc(const DenseArgs& a, float* delta, cudaStream_t st) {
+int launch_dense_bwd_tc(const DenseArgs& a, float* delta, float* parts, cudaStream_t st) {
     if (a.Nq == 0 && a.Nk == 0) return PARK_OK;
     CUtensorMap m[4];
     const Op4* ops[4] = {&a.q, &a.d_o, &a.k, &a.v};
@@ -713,7 +727,7 @@ int launch_dense_bwd_tc(const DenseArgs& a, float* delta, cudaStream_t st) {
         PARK_CHECK(map_4d(&m[i], op, empty ? 1 : a.B, empty ? 1 : qs ? a.Hq : a.Hk, empty ? 1 : qs ? a.Nq : a.Nk, a.D,
                           kTile));
     }
-    return a.D <= 64 ? bwd_tc<1>(a, m, delta, st) : bwd_tc<2>(a, m, delta, st);
+    return a.D <= 64 ? bwd_tc<1>(a, m, delta, parts, st) : bwd_tc<2>(a, m, delta, parts, st);
 }
 
 }  // namespace park

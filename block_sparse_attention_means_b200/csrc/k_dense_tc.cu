@@ -431,45 +431,6 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0 && sh.abort) set_status(a.status, PARK_ERR_TIMEOUT);
 }
 
-// Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum; one warp a row.
-__global__ void __launch_bounds__(256)
-    k_dense_combine(DenseArgs a, int n_split, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
-    const int lane = threadIdx.x & 31, G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
-    const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (x >= a.Nq * G) return;
-    const SeqTile t = dense_resolve(a, x, 1, false, G);  // tiles of one row
-    if (!t.live) return;
-    const float NI = __int_as_float(0xff800000);
-    const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
-    const int tok = t.tile / G, head = hk * G + (t.tile - tok * G);
-    const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
-    float M = NI;
-    for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
-    M = warp_max(M);
-    const bool none = M == NI;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < n_split; ++s) {
-        const float ls = part_lse[s * rows_all + id];
-        if (ls == NI) continue;  // (its part of o may not be written)
-        const float w = ex2(ls - M);
-        sum += w;
-        if (4 * lane < a.D) {
-            const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
-            acc.x = fmaf(w, o.x, acc.x);
-            acc.y = fmaf(w, o.y, acc.y);
-            acc.z = fmaf(w, o.z, acc.z);
-            acc.w = fmaf(w, o.w, acc.w);
-        }
-    }
-    const float inv = none ? 0.f : 1.f / sum;
-    if (4 * lane < a.D)
-        *reinterpret_cast<uint2*>(a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2 + 8 * lane) =
-            make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-    if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
-}
-
 template <int NP>
 int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, const DenseSplit& sp, float* part_o,
            float* part_lse, cudaStream_t st) {
@@ -483,30 +444,8 @@ int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, con
 
 }  // namespace
 
-DenseSplit dense_split(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
-    DenseSplit s;
-    s.tiles = dense_tiles(Nq * (Hq / Hk), n_seq, 2 * kTile);
-    s.n = 1;
-    s.chunk = 0;
-    const long long kt = (Nk + kTile - 1) / kTile + (n_seq > 0 ? n_seq : 0), ctas = s.tiles * Hk * B;
-    if (ctas * 2 <= kDenseSMs && kt > 8) {
-        // Parts of equal length whatever the sequence (a packed batch holds at most kt key tiles in
-        // all, one of a batch's entries as many), about two waves of them, at least 4 tiles each.
-        const long long work = (n_seq > 0 ? kt : kt * B) * Hk * (n_seq > 0 ? 1 : s.tiles);
-        long long chunk = (work + 2 * kDenseSMs - 1) / (2 * kDenseSMs);
-        if (chunk < 4) chunk = 4;
-        s.n = (int)((kt + chunk - 1) / chunk);
-        s.chunk = (int)chunk;
-        if (s.n <= 1) s.n = 1;
-    }
-    const size_t rows = (size_t)B * Hq * Nq;
-    s.lse_off = s.n > 1 ? align_up((size_t)s.n * rows * D * 4, 256) : 0;
-    s.bytes = s.n > 1 ? s.lse_off + align_up((size_t)s.n * rows * 4, 256) : 0;
-    return s;
-}
-
 int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
-    const DenseSplit sp = dense_split(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
+    const DenseSplit sp = dense_split_tc(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
     if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
     CUtensorMap mK, mV;
     // without keys nothing is loaded; the maps still have to be valid
@@ -516,11 +455,7 @@ int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
     float* part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sp.lse_off);
     PARK_CHECK(a.D <= 64 ? fwd_tc<1>(a, mK, mV, sp, part_o, part_lse, st)
                          : fwd_tc<2>(a, mK, mV, sp, part_o, part_lse, st));
-    if (sp.n == 1) return PARK_OK;
-    ::park::prof_begin(st);
-    k_dense_combine<<<dim3((unsigned)((a.Nq * (a.Hq / a.Hk) + 7) / 8), a.Hk, a.B), 256, 0, st>>>(a, sp.n, part_o, part_lse);
-    PARK_TRY_LAUNCH("k_dense_combine", st);
-    return PARK_OK;
+    return sp.n > 1 ? launch_dense_combine(a, PARK_BF16, sp.n, part_o, part_lse, st) : PARK_OK;
 }
 
 }  // namespace park

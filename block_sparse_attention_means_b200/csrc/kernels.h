@@ -212,14 +212,22 @@ int launch_norm_rope_bwd(const park_operand* dyq, const park_operand* dyk, const
 
 // ---- k_dense.cu: dense attention (bounds and operands as in dense.cuh)
 struct DenseArgs;
-int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st);
-int launch_dense_fwd_simt(const DenseArgs& a, cudaStream_t st);  // float32
-int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, cudaStream_t st);
-// ---- k_dense_tc.cu: bf16 on tcgen05
 struct DenseSplit;
-DenseSplit dense_split(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D);
+DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D);    // bf16
+DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D);  // float32
+int launch_dense_combine(const DenseArgs& a, int dtype, int n_split, const float* part_o, const float* part_lse,
+                         cudaStream_t st);
+struct DkvSplit;
+// tile: rows and keys of a tile (128: bf16, 64: float32)
+DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D, int tile);
+int launch_dense_dkv_reduce(const DenseArgs& a, int dtype, const DkvSplit& sp, int tile, const float* dv, const float* dk,
+                            cudaStream_t st);
+int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st);
+int launch_dense_fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st);  // float32
+int launch_dense_bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t st);
+// ---- k_dense_tc.cu: bf16 on tcgen05
 int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st);
-int launch_dense_bwd_tc(const DenseArgs& a, float* delta, cudaStream_t st);  // k_dense_bwd_tc.cu; corrects delta
+int launch_dense_bwd_tc(const DenseArgs& a, float* delta, float* parts, cudaStream_t st);  // k_dense_bwd_tc.cu; corrects delta
 int make_tma_map_4d(CUtensorMap* map, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
                     const cuuint32_t* box);
 

@@ -131,9 +131,10 @@ size_t delta_bytes(const park_attn_shape* s, int Hq) { return align_up((size_t)s
 
 int attn_workspace(const park_attn_shape* s, int Hq, int Hk, int backward, size_t* bytes) {
     if (backward)
-        *bytes = delta_bytes(s, Hq);
+        *bytes = delta_bytes(s, Hq) +
+                 dense_split_dkv(s->B, Hq, Hk, s->Nq, s->Nk, s->n_seq, s->D, s->dtype == PARK_BF16 ? 128 : 64).bytes;
     else
-        *bytes = s->dtype == PARK_BF16 ? dense_split(s->B, Hq, Hk, s->Nq, s->Nk, s->n_seq, s->D).bytes : 0;
+        *bytes = (s->dtype == PARK_BF16 ? dense_split_tc : dense_split_simt)(s->B, Hq, Hk, s->Nq, s->Nk, s->n_seq, s->D).bytes;
     return PARK_OK;
 }
 
@@ -245,7 +246,7 @@ int park_attention(const park_attn_shape* shape, const park_operand* q, const pa
     if (s->Nq == 0) return PARK_OK;
     const DenseArgs a = dense_args(s, q, k, v, o, lse, status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return s->dtype == PARK_BF16 ? launch_dense_fwd_tc(a, ws, st) : launch_dense_fwd_simt(a, st);
+    return s->dtype == PARK_BF16 ? launch_dense_fwd_tc(a, ws, st) : launch_dense_fwd_simt(a, ws, st);
 }
 
 int park_attention_bwd(const park_attn_shape* shape, const park_operand* d_o, const park_operand* q,
@@ -275,7 +276,8 @@ int park_attention_bwd(const park_attn_shape* shape, const park_operand* d_o, co
     float* delta = static_cast<float*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s->Nq > 0) PARK_CHECK(launch_dense_delta(a, s->dtype, delta, st));
-    return s->dtype == PARK_BF16 ? launch_dense_bwd_tc(a, delta, st) : launch_dense_bwd_simt(a, delta, st);
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + delta_bytes(s, q->H));
+    return s->dtype == PARK_BF16 ? launch_dense_bwd_tc(a, delta, parts, st) : launch_dense_bwd_simt(a, delta, parts, st);
 }
 
 }  // extern "C"

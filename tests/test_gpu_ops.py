@@ -435,6 +435,10 @@ def test_attention_batched(B, Hq, Hk, Nq, Nk, D, causal, dt, kind):
 
 
 PACKED = [
+    (4, 2, [1500, 3, 700], [77, 200, 1], 128, False, BF, "tokens"),       # many rows over few keys: split over the rows
+    (2, 1, [1500, 0, 900, 130], [60, 10, 1000, 0], 64, True, BF, "heads"),
+    (4, 2, [900, 3, 400], [77, 100, 1], 96, False, F32, "tokens"),
+    (2, 1, [5, 1, 40, 2], [900, 300, 1, 0], 128, True, F32, "heads"),     # few rows over many keys in float32
     # Hq, Hk, lq, lk, D, causal, dtype, layout
     (4, 2, [5, 0, 131, 1, 64, 300], [5, 0, 131, 1, 64, 300], 128, True, BF, "tokens"),
     (2, 1, [17, 3, 0, 200], [0, 140, 9, 33], 64, True, BF, "heads"),      # no keys, no queries, more queries than keys
