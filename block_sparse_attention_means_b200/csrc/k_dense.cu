@@ -23,19 +23,9 @@ namespace {
 constexpr int TB = 64;          // query rows and key rows of a tile
 constexpr int PP = TB + 4;      // row pitch of a probability tile
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const uint8_t* p, int i);
-template <>
-__device__ __forceinline__ float4 load4<float>(const uint8_t* p, int i) {
+__device__ __forceinline__ float4 load4(const uint8_t* p, int i) {
     return *reinterpret_cast<const float4*>(p + 16 * (size_t)i);
 }
-template <>
-__device__ __forceinline__ float4 load4<bf16_t>(const uint8_t* p, int i) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * (size_t)i);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
-}
-
 // rows 0 .. n-1 of `src` (row stride in elements) into a [ROWS][D + 4] tile, zeros below
 template <int D, int ROWS>
 __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long long stride, int n) {
@@ -43,7 +33,7 @@ __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long l
     for (int i = threadIdx.x; i < ROWS * C; i += 256) {
         const int r = i / C, c = i - r * C;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) v = load4<float>(src + r * stride * 4, c);
+        if (r < n) v = load4(src + r * stride * 4, c);
         *reinterpret_cast<float4*>(dst + r * (D + 4) + 4 * c) = v;
     }
 }
@@ -159,7 +149,7 @@ __global__ void __launch_bounds__(256)
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int tok = (r0 + r) / G, h = hk * G + (r0 + r - tok * G);
-                v = load4<float>(row_ptr<float>(a.q, b, h, t.q0 + tok), c);
+                v = load4(row_ptr<float>(a.q, b, h, t.q0 + tok), c);
             }
             *reinterpret_cast<float4*>(Qs + r * (D + 4) + 4 * c) = v;
         }
@@ -247,15 +237,18 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum; one warp a row.
-template <typename T>
+// Joins the parts of a split: o = sum_s w_s o_s, w_s = 2^(lse_s - M) / sum.  W warps share a row's parts (few rows have many
+// parts, many rows few).
+template <typename T, int W>
 __global__ void __launch_bounds__(256)
     k_dense_combine(DenseArgs a, int n_split, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
-    const int lane = threadIdx.x & 31, G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
-    const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
+    __shared__ float4 sh_o[W][32];
+    __shared__ float sh_sum[W];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hk, hk = blockIdx.y, b = blockIdx.z;
+    const int x = W == 1 ? blockIdx.x * 8 + warp : blockIdx.x, w0 = W == 1 ? 0 : warp;
     if (x >= a.Nq * G) return;
     const SeqTile t = dense_resolve(a, x, 1, false, G);  // tiles of one row
-    if (!t.live) return;
+    if (!t.live) return;                                 // (alike in all warps of a row)
     const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
     const int tok = t.tile / G, head = hk * G + (t.tile - tok * G);
     const size_t id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
@@ -266,7 +259,7 @@ __global__ void __launch_bounds__(256)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < n_split; ++s) {
+    for (int s = w0; s < n_split; s += W) {
         const float ls = part_lse[s * rows_all + id];
         if (ls == -INFINITY) continue;  // (its part of o may not be written)
         const float w = exp2f(ls - M);
@@ -279,27 +272,56 @@ __global__ void __launch_bounds__(256)
             acc.w = fmaf(w, o.w, acc.w);
         }
     }
+    if (W > 1) {
+        sh_o[w0][lane] = acc;
+        if (lane == 0) sh_sum[w0] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int i = 1; i < W; ++i) {
+            const float4 o = sh_o[i][lane];
+            acc = make_float4(acc.x + o.x, acc.y + o.y, acc.z + o.z, acc.w + o.w);
+            sum += sh_sum[i];
+        }
+    }
     const float inv = none ? 0.f : 1.f / sum;
     if (4 * lane < a.D)
         store4<T>(row_ptr<T>(a.o, b, head, t.q0 + tok), lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     if (a.lse && lane == 0) a.lse[id] = none ? M : (M + log2f(sum)) * kLn2;
 }
 
-// delta [B, Hq, Nq]: one warp a row
+// delta [B, Hq, Nq].  16 bytes a lane, 8 lanes a row up to 128 bytes and 16 or 32 above; four rows of a lane in flight.
 template <typename T>
 __global__ void __launch_bounds__(256) k_dense_delta(DenseArgs a, float* __restrict__ delta) {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)a.B * a.Hq * a.Nq) return;
-    const long long n = row % a.Nq, bh = row / a.Nq;
-    const int h = (int)(bh % a.Hq), b = (int)(bh / a.Hq);
-    float s = 0.f;
-    if (4 * lane < a.D) {
-        const float4 x = load4<T>(row_ptr<T>(a.o, b, h, n), lane), y = load4<T>(row_ptr<T>(a.d_o, b, h, n), lane);
-        s = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+    constexpr int E = 16 / sizeof(T);
+    const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
+    const int lpr = a.D <= 8 * E ? 8 : (a.D <= 16 * E ? 16 : 32), rpw = 32 / lpr, l = lane % lpr;
+    const bool on = l * E < a.D;
+    const long long n0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * rpw * 4 + lane / lpr;
+    const uint8_t *po = row_ptr<T>(a.o, b, h, n0) + 16 * l, *pg = row_ptr<T>(a.d_o, b, h, n0) + 16 * l;
+    uint4 o[4], g[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        o[u] = g[u] = make_uint4(0, 0, 0, 0);
+        if (on && n0 + u * rpw < a.Nq) {
+            o[u] = __ldg(reinterpret_cast<const uint4*>(po + u * rpw * a.o.sn * (long long)sizeof(T)));
+            g[u] = __ldg(reinterpret_cast<const uint4*>(pg + u * rpw * a.d_o.sn * (long long)sizeof(T)));
+        }
     }
-    s = warp_sum(s);
-    if (lane == 0) delta[row] = s;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t x[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, y[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (sizeof(T) == 4)
+                s = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), s);
+            else
+                s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16),
+                         fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), s));
+        }
+        for (int d = lpr / 2; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (l == 0 && n0 + u * rpw < a.Nq) delta[((size_t)b * a.Hq + h) * a.Nq + n0 + u * rpw] = s;
+    }
 }
 
 template <int D>
@@ -530,12 +552,17 @@ int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t 
 
 int launch_dense_combine(const DenseArgs& a, int dtype, int n_split, const float* part_o, const float* part_lse,
                          cudaStream_t st) {
-    const dim3 grid((unsigned)((a.Nq * (a.Hq / a.Hk) + 7) / 8), a.Hk, a.B);
+    const long long rows = a.Nq * (a.Hq / a.Hk);
+    const bool wide = n_split > 4;
+    const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8), a.Hk, a.B);
     ::park::prof_begin(st);
-    if (dtype == PARK_BF16)
-        k_dense_combine<bf16_t><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
-    else
-        k_dense_combine<float><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+    if (dtype == PARK_BF16) {
+        if (wide) k_dense_combine<bf16_t, 8><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+        else k_dense_combine<bf16_t, 1><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+    } else {
+        if (wide) k_dense_combine<float, 8><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+        else k_dense_combine<float, 1><<<grid, 256, 0, st>>>(a, n_split, part_o, part_lse);
+    }
     PARK_TRY_LAUNCH("k_dense_combine", st);
     return PARK_OK;
 }
@@ -597,9 +624,13 @@ static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long 
 }
 
 DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
+    // 256 rows and one CTA an SM, or, where those CTAs would fill no more than half of the SMs, 128 rows and two CTAs an SM
+    // (8 heads x 2,048^2: 39 us against 60 with split keys; 300 x 20,000 keys 58 against 73; where both fill the GPU 256
+    // rows are faster: 8 heads x 16,384^2 0.88 ms against 1.02, D = 64 0.78 against 0.89)
     DenseSplit s;
-    s.rows = 256;
-    s.tiles = dense_tiles(Nq * (Hq / Hk), n_seq, s.rows);
+    const long long rows = Nq * (Hq / Hk);
+    s.rows = dense_tiles(rows, n_seq, 256) * Hk * B * 2 <= kDenseSMs ? 128 : 256;
+    s.tiles = dense_tiles(rows, n_seq, s.rows);
     split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 4);
     return s;
 }
@@ -621,13 +652,13 @@ DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, i
 }
 
 int launch_dense_delta(const DenseArgs& a, int dtype, float* delta, cudaStream_t st) {
-    const long long rows = (long long)a.B * a.Hq * a.Nq;
-    const unsigned blocks = (unsigned)((rows + 7) / 8);
+    const int E = dtype == PARK_BF16 ? 8 : 4, lpr = a.D <= 8 * E ? 8 : (a.D <= 16 * E ? 16 : 32), rows = 32 / lpr * 4 * 8;
+    const dim3 grid((unsigned)((a.Nq + rows - 1) / rows), a.Hq, a.B);
     ::park::prof_begin(st);
     if (dtype == PARK_BF16)
-        k_dense_delta<bf16_t><<<blocks, 256, 0, st>>>(a, delta);
+        k_dense_delta<bf16_t><<<grid, 256, 0, st>>>(a, delta);
     else
-        k_dense_delta<float><<<blocks, 256, 0, st>>>(a, delta);
+        k_dense_delta<float><<<grid, 256, 0, st>>>(a, delta);
     PARK_TRY_LAUNCH("k_dense_delta", st);
     return PARK_OK;
 }

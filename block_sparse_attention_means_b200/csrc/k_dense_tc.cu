@@ -39,11 +39,19 @@ namespace {
 
 constexpr float kRescale = 8.f;        // log2 units
 
-template <int NP>
-struct FwdCfg {  // NP: 64-column panels of the padded head dimension
-    static constexpr int KS = NP == 2 ? 3 : 4, VS = NP == 2 ? 2 : 4;  // ring stages of K, of V
+// NP: 64-column panels of the padded head dimension.  NS: 128-row stages of a CTA.  Two stages share each K and V tile and
+// one CTA fills an SM; one stage leaves room for a second CTA, whose work covers this one's start and end.
+template <int NP, int NS>
+struct FwdCfg {
+    static constexpr int KS = NS == 2 ? (NP == 2 ? 3 : 4) : (NP == 2 ? 1 : 2);  // ring stages of K
+    static constexpr int VS = NS == 2 ? (NP == 2 ? 2 : 4) : (NP == 2 ? 1 : 2);  // and of V
     static constexpr uint32_t tile = NP * kPanel;
-    static constexpr size_t smem = (size_t)(2 + KS + VS) * tile + 1024;
+    static constexpr size_t smem = (size_t)(NS + KS + VS) * tile + 1024;
+    static constexpr int threads = 128 * NS + 128, ctas = NS == 2 ? 1 : 2;
+    static constexpr int tmem_cols = NS == 2 ? 512 : 256, O = 128 * NS;  // S_0 (S_1) O_0 (O_1)
+    // registers of a Softmax thread and of the others: 256 x 216 + 128 x 56 of the 384 x 168 that a launch of two stages
+    // holds, 128 x 200 + 128 x 56 = 256 x 128 of one
+    static constexpr int soft_regs = NS == 2 ? 216 : 200, misc_regs = 56;
 };
 
 struct FwdSmem {
@@ -59,47 +67,77 @@ struct FwdSmem {
 __device__ constexpr bool poly_pair(int e) { return e % 4 == 0; }
 
 // The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
-struct Piece {
-    int r0, rows, nt[2], j_lo, jmax;
+// Row of a group's rows -> token (a division only where heads share keys).
+__device__ __forceinline__ int token_of(int r, int G) { return G == 1 ? r : r / G; }
+
+// Walks rows r, r + RS, r + 2 RS .. of a tensor whose rows are counted token by token, heads side by side: offset of the
+// row from the first head's first token, in bytes.
+template <int RS>
+struct RowWalk {
+    int g, G, dg;
+    long long at, step, carry;
+    __device__ __forceinline__ RowWalk(int r, int G_, long long sh, long long sn) : G(G_) {
+        const int tk = token_of(r, G), q = G == 1 ? RS : RS / G;
+        g = r - tk * G;
+        dg = RS - q * G;
+        at = (tk * sn + g * sh) * 2;
+        step = (q * sn + dg * sh) * 2;
+        carry = (sn - G * sh) * 2;
+    }
+    __device__ __forceinline__ void next() {
+        at += step;
+        g += dg;
+        if (g >= G) {
+            g -= G;
+            at += carry;
+        }
+    }
 };
-__device__ __forceinline__ Piece fwd_piece(const SeqTile& t, int G, int causal, int n_split, int sp, int chunk) {
-    Piece p;
-    p.r0 = t.tile * 2 * kTile;
-    p.rows = t.live ? min(2 * kTile, t.nq * G - p.r0) : 0;
+
+template <int NS>
+struct Piece {
+    int r0, rows, nt[NS], j_lo, jmax;
+};
+template <int NS>
+__device__ __forceinline__ Piece<NS> fwd_piece(const SeqTile& t, int G, int causal, int n_split, int sp, int chunk) {
+    Piece<NS> p;
+    p.r0 = t.tile * NS * kTile;
+    p.rows = t.live ? min(NS * kTile, t.nq * G - p.r0) : 0;
+    p.jmax = 0;
     p.j_lo = n_split > 1 ? sp * chunk : 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < NS; ++s) {
         const int last = min(p.rows, (s + 1) * kTile) - 1;  // last row of the stage
         int n = 0;
         if (last >= s * kTile) {
-            const int kend = dense_last_key((p.r0 + last) / G, t.nq, t.nk, causal) + 1;
+            const int kend = dense_last_key(token_of(p.r0 + last, G), t.nq, t.nk, causal) + 1;
             n = kend > 0 ? (kend + kTile - 1) / kTile : 0;
             n = max(0, (n_split > 1 ? min(n, p.j_lo + chunk) : n) - p.j_lo);
         }
         p.nt[s] = n;
+        p.jmax = max(p.jmax, n);
     }
-    p.jmax = max(p.nt[0], p.nt[1]);
     return p;
 }
 
-template <int NP>
-__global__ void __launch_bounds__(384, 1)
+template <int NP, int NS>
+__global__ void __launch_bounds__(FwdCfg<NP, NS>::threads, FwdCfg<NP, NS>::ctas)
     k_dense_fwd_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
                    int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse, uint64_t wait_ns) {
-    using C = FwdCfg<NP>;
+    using C = FwdCfg<NP, NS>;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     __shared__ FwdSmem sh;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-    uint8_t* Qs = base;                 // two tiles
-    uint8_t* Ks = base + 2 * C::tile;   // rings
+    uint8_t* Qs = base;                 // NS tiles
+    uint8_t* Ks = base + NS * C::tile;  // rings
     uint8_t* Vs = Ks + C::KS * C::tile;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
     if (warp == 0) {
-        const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, 2 * kTile, false, a.Hq / a.Hk);
+        const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, NS * kTile, false, a.Hq / a.Hk);
         if (lane == 0) {
             sh.seq = t;
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < NS; ++s) {
                 mbar_init(&sh.q_full[s], 128);
                 mbar_init(&sh.s_full[s], 1);
                 mbar_init(&sh.p_full[s][0], 128);
@@ -120,8 +158,8 @@ __global__ void __launch_bounds__(384, 1)
             sh.poison = 0;
             mbar_fence_init();
         }
-    } else if (warp == 9) {
-        tmem_alloc(&sh.tmem_base, 512);
+    } else if (warp == 4 * NS + 1) {
+        tmem_alloc(&sh.tmem_base, C::tmem_cols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -131,13 +169,13 @@ __global__ void __launch_bounds__(384, 1)
     const SeqTile t = sh.seq;
     const int G = a.Hq / a.Hk, hk = blockIdx.y;
     const int b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split;
-    const Piece pc = fwd_piece(t, G, a.causal, n_split, sp, chunk);
+    const Piece<NS> pc = fwd_piece<NS>(t, G, a.causal, n_split, sp, chunk);
     // first key tile (counted within the piece) that some row does not see whole
-    const int cut = (dense_last_key(pc.r0 / G, t.nq, t.nk, a.causal) + 1) / kTile - pc.j_lo;
+    const int cut = (dense_last_key(token_of(pc.r0, G), t.nq, t.nk, a.causal) + 1) / kTile - pc.j_lo;
 
-    if (warp >= 8) {
-        reg_dec<56>();
-        if (warp == 8 && lane == 0) {
+    if (warp >= 4 * NS) {
+        reg_dec<C::misc_regs>();
+        if (warp == 4 * NS && lane == 0) {
             // ---------------------------------------------------------------- TMA
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
@@ -161,7 +199,7 @@ __global__ void __launch_bounds__(384, 1)
                 wait_bar(&sh.k_full[j % C::KS], (j / C::KS) & 1, &dummy, 100000000ull);
             for (int j = max(0, nv - C::VS); j < nv; ++j)
                 wait_bar(&sh.v_full[j % C::VS], (j / C::VS) & 1, &dummy, 100000000ull);
-        } else if (warp == 9) {
+        } else if (warp == 4 * NS + 1) {
             // ---------------------------------------------------------------- MMA
             const uint32_t idS = idesc_bf16(128, 128, 0, 0), idO = idesc_bf16(128, 64 * NP, 0, 1);
             const bool lead = elect_one();
@@ -181,13 +219,13 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     umma_commit(&sh.s_full[s]);
                     // the last stage that uses K_j frees it
-                    if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.k_empty[st]);
+                    if (s == NS - 1 || pc.nt[NS - 1] <= j) umma_commit(&sh.k_empty[st]);
                 }
                 __syncwarp();
                 return true;
             };
             bool ok = true;
-            for (int s = 0; s < 2 && ok; ++s)
+            for (int s = 0; s < NS && ok; ++s)
                 if (pc.nt[s] > 0) {
                     ok = wait_warp(&sh.q_full[s], 0, abort, wait_ns);
                     if (ok) ok = issue_S(s, 0);
@@ -196,7 +234,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int st = j % C::VS;
                 const uint64_t va = dV + ((st * C::tile) >> 4);
                 if (!wait_warp(&sh.v_clean[st], (j / C::VS) & 1, abort, wait_ns)) break;
-                for (int s = 0; s < 2 && ok; ++s) {
+                for (int s = 0; s < NS && ok; ++s) {
                     if (j >= pc.nt[s]) continue;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -208,7 +246,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (lead) {
 #pragma unroll
                             for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                umma_bf16_ts(tm + 256 + 64 * NP * s, tm + 128 * s + 8 * kk, va + ((kk * 2048) >> 4), idO,
+                                umma_bf16_ts(tm + C::O + 64 * NP * s, tm + 128 * s + 8 * kk, va + ((kk * 2048) >> 4), idO,
                                              j > 0 || kk > 0);
                         }
                         __syncwarp();
@@ -216,7 +254,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (!ok) break;
                     if (lead) {
                         if (j + 1 == pc.nt[s]) umma_commit(&sh.o_full[s]);
-                        if (s == 1 || pc.nt[1] <= j) umma_commit(&sh.v_empty[st]);
+                        if (s == NS - 1 || pc.nt[NS - 1] <= j) umma_commit(&sh.v_empty[st]);
                     }
                     __syncwarp();
                     if (j + 1 < pc.nt[s]) ok = issue_S(s, j + 1);
@@ -226,7 +264,7 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             int dummy = 0;
             wait_bar(&sh.final_bar, 0, &dummy, 100000000ull);
-        } else if (warp == 10) {
+        } else if (warp == 4 * NS + 2) {
             // ---------------------------------------------------------------- V tiles: forward, clean where cut
             for (int j = 0; j < pc.jmax; ++j) {
                 const int st = j % C::VS;
@@ -248,38 +286,37 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------------------- Softmax
-        reg_inc<216>();
+        reg_inc<C::soft_regs>();
         const int s = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
         const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
-        const uint32_t scol = trow + 128 * s, ocol = trow + 256 + 64 * NP * s;
+        const uint32_t scol = trow + 128 * s, ocol = trow + C::O + 64 * NP * s;
         const int nt = pc.nt[s];
-        const int r = pc.r0 + kTile * s + row;
-        const int tok = r / G, head = hk * G + (r - tok * G);
         const bool live = kTile * s + row < pc.rows;
-        constexpr int PR = 8 * NP;  // 16-byte pieces of a row
+        // The warp's 32 rows move 16 bytes a lane: piece `pc16` of row (lane / PR) and of every (32 / PR)-th row after it.
+        constexpr int PR = 8 * NP, RS = 32 / PR;  // pieces of a row, rows of a step
         uint8_t* qt = Qs + s * C::tile;
-        const int chunks = a.D / 8;
+        const int pc16 = lane % PR, row0 = kTile * s + 32 * quad + lane / PR;
+        const bool piece = pc16 < a.D / 8;
         if (nt > 0) {
-            // the warp's 32 query rows into the swizzled tile, all loads in flight at once
-            uint8_t* src = live ? a.q.p + (b * a.q.sb + head * a.q.sh + (t.q0 + tok) * a.q.sn) * 2 : nullptr;
-            uint4 v[PR];
-#pragma unroll
+            RowWalk<RS> w(pc.r0 + row0, G, a.q.sh, a.q.sn);
+            const uint8_t* qb = a.q.p + (b * a.q.sb + hk * (long long)G * a.q.sh + t.q0 * a.q.sn) * 2 + 16 * pc16;
+            const uint32_t dst = smem_u32(qt) + (pc16 >> 3) * kPanel;
+#pragma unroll 4
             for (int i = 0; i < PR; ++i) {
-                const int e = 32 * i + lane;
-                const uint8_t* row_src = shfl_ptr(src, e / PR);
-                v[i] = row_src && e % PR < chunks ? __ldg(reinterpret_cast<const uint4*>(row_src) + e % PR) : make_uint4(0, 0, 0, 0);
+                const int rr = 32 * quad + lane / PR + i * RS;
+                const bool on = piece && row0 + i * RS < pc.rows;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((pc16 & 7) ^ (rr & 7)) << 4)),
+                             "l"(qb + (on ? w.at : 0)), "r"(on ? 16 : 0)
+                             : "memory");  // (0 bytes read: zeros)
+                w.next();
             }
-#pragma unroll
-            for (int i = 0; i < PR; ++i) {
-                const int e = 32 * i + lane, rr = 32 * quad + e / PR, c = e % PR;
-                *reinterpret_cast<uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[i];
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full[s]);
         }
         const float sl2 = a.scale * kLog2e, NI = __int_as_float(0xff800000);
         const float2 sl22 = make_float2(sl2, sl2);
-        const int seen = live ? dense_last_key(tok, t.nq, t.nk, a.causal) : -1;  // last visible key
+        const int seen = live ? dense_last_key(token_of(pc.r0 + kTile * s + row, G), t.nq, t.nk, a.causal) : -1;  // last visible key
         float m = NI;
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool ok = true;
@@ -355,8 +392,8 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             int r = pc.r0 + kTile * s + row;  // (formed again: nothing of it has to live through the loop)
             asm volatile("" : "+r"(r));
-            const int tok = r / G, head = hk * G + (r - tok * G);
-            const bool live = kTile * s + row < pc.rows;
+            const int tok = token_of(r, G), head = hk * G + (r - tok * G);
+            const bool poison = sh.poison != 0;
             const bool none = m == NI && l == 0.f;  // no visible key (or every score -inf)
             const float inv = none ? 0.f : 1.f / l;
             const size_t row_id = ((size_t)b * a.Hq + head) * a.Nq + t.q0 + tok;
@@ -369,22 +406,27 @@ __global__ void __launch_bounds__(384, 1)
                 else if (a.lse)
                     a.lse[row_id] = lse * kLn2;
             }
-            uint8_t* orow = a.o.p + (b * a.o.sb + head * a.o.sh + (t.q0 + tok) * a.o.sn) * 2;
             float* prow = part_o + (sp * rows_all + row_id) * a.D;
             if (!(split && nt == 0)) {  // (a part without keys is only its lse)
-#pragma unroll
-                for (int c = 0; c < 2 * NP; ++c) {
-                    if (32 * c >= a.D) break;
+#pragma unroll 1
+                for (int c = 0; 32 * c < a.D; ++c) {
                     uint32_t o[32];
                     __syncwarp();
                     if (nt > 0) {
                         tmem_ld32(ocol + 32 * c, o);
                         tmem_ld_wait();
                         tmem_ld_dep(o);
-                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = nt > 0 && !none ? __float_as_uint(f_of(o[e]) * inv) : 0u;
-                    if (sh.poison && live) {  // infinities and NaN that the row does see in the cut tiles
+                        for (int e = 0; e < 32; e += 2) {  // (rows without a key: O = 0, inv = 0)
+                            const float2 x = __fmul2_rn(make_float2(f_of(o[e]), f_of(o[e + 1])), make_float2(inv, inv));
+                            o[e] = __float_as_uint(x.x);
+                            o[e + 1] = __float_as_uint(x.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (poison && live) {  // infinities and NaN that the row does see in the cut tiles
                         const int k1 = min(seen + 1, (pc.j_lo + nt) * kTile);
                         for (int key = max(0, pc.j_lo + cut) * kTile; key < k1; ++key) {
                             const uint16_t* vr = reinterpret_cast<const uint16_t*>(
@@ -409,35 +451,37 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
             }
-            if (!split) {  // whole rows, 16 bytes a lane
+            if (!split) {  // whole rows
                 __syncwarp();
-                uint8_t* dst = live ? orow : nullptr;
-#pragma unroll
+                RowWalk<RS> w(pc.r0 + row0, G, a.o.sh, a.o.sn);
+                uint8_t* ob = a.o.p + (b * a.o.sb + hk * (long long)G * a.o.sh + t.q0 * a.o.sn) * 2 + 16 * pc16;
+#pragma unroll 4
                 for (int i = 0; i < PR; ++i) {
-                    const int e = 32 * i + lane, rr = 32 * quad + e / PR, c = e % PR;
-                    uint8_t* row_dst = shfl_ptr(dst, e / PR);
-                    const uint4 v = *reinterpret_cast<const uint4*>(qt + (c >> 3) * kPanel + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
-                    if (row_dst && c < chunks) *(reinterpret_cast<uint4*>(row_dst) + c) = v;
+                    const int rr = 32 * quad + lane / PR + i * RS;
+                    const uint4 v = *reinterpret_cast<const uint4*>(qt + (pc16 >> 3) * kPanel + rr * 128 + (((pc16 & 7) ^ (rr & 7)) << 4));
+                    if (piece && row0 + i * RS < pc.rows) *reinterpret_cast<uint4*>(ob + w.at) = v;
+                    w.next();
                 }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 4 * NS + 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, C::tmem_cols);
     }
     if (threadIdx.x == 0 && sh.abort) set_status(a.status, PARK_ERR_TIMEOUT);
 }
 
-template <int NP>
+template <int NP, int NS>
 int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, const DenseSplit& sp, float* part_o,
            float* part_lse, cudaStream_t st) {
-    cudaFuncSetAttribute(k_dense_fwd_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdCfg<NP>::smem);
+    using C = FwdCfg<NP, NS>;
+    cudaFuncSetAttribute(k_dense_fwd_tc<NP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
     const dim3 grid((unsigned)sp.tiles, a.Hk, a.B * sp.n);
     ::park::prof_begin(st);
-    k_dense_fwd_tc<NP><<<grid, 384, FwdCfg<NP>::smem, st>>>(mK, mV, a, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
+    k_dense_fwd_tc<NP, NS><<<grid, C::threads, C::smem, st>>>(mK, mV, a, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
     PARK_TRY_LAUNCH("k_dense_fwd_tc", st);
     return PARK_OK;
 }
@@ -453,8 +497,10 @@ int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
     PARK_CHECK(map_4d(&mV, a.Nk ? a.v : a.q, a.Nk ? a.B : 1, a.Nk ? a.Hk : 1, a.Nk ? a.Nk : 1, a.D, kTile));
     float* part_o = static_cast<float*>(ws);
     float* part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sp.lse_off);
-    PARK_CHECK(a.D <= 64 ? fwd_tc<1>(a, mK, mV, sp, part_o, part_lse, st)
-                         : fwd_tc<2>(a, mK, mV, sp, part_o, part_lse, st));
+    PARK_CHECK(sp.rows == 256 ? (a.D <= 64 ? fwd_tc<1, 2>(a, mK, mV, sp, part_o, part_lse, st)
+                                           : fwd_tc<2, 2>(a, mK, mV, sp, part_o, part_lse, st))
+                              : (a.D <= 64 ? fwd_tc<1, 1>(a, mK, mV, sp, part_o, part_lse, st)
+                                           : fwd_tc<2, 1>(a, mK, mV, sp, part_o, part_lse, st)));
     return sp.n > 1 ? launch_dense_combine(a, PARK_BF16, sp.n, part_o, part_lse, st) : PARK_OK;
 }
 
