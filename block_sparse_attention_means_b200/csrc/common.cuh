@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "park.h"
 
 namespace park {
@@ -35,6 +37,19 @@ void prof_end(const char* name, cudaStream_t st);
         int _rc = (x);                    \
         if (_rc != PARK_OK) return _rc;   \
     } while (0)
+
+// Raises a kernel's dynamic shared memory limit, once for each device.
+template <typename K>
+inline void allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    else
+        cudaGetLastError();  // (the launch reports it)
+}
 
 static inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -509,7 +509,10 @@ __global__ void __launch_bounds__(256)
 template <int D, int R>
 int fwd_simt_r(const DenseArgs& a, const DenseSplit& sp, float* part_o, float* part_lse, cudaStream_t st) {
     const size_t sm = (size_t)((16 * R + 2 * TB) * (D + 4) + 16 * R * PP) * 4;
-    cudaFuncSetAttribute(k_dense_fwd_simt<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_fwd_simt<D, R>, sm, done);
+    }
     ::park::prof_begin(st);
     k_dense_fwd_simt<D, R><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 256, sm, st>>>(a, sp.n, sp.chunk, part_o, part_lse);
     PARK_TRY_LAUNCH("k_dense_fwd_simt", st);
@@ -531,8 +534,14 @@ int fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st) {
 template <int D>
 int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t st) {
     const size_t sq = (size_t)(4 * TB * (D + 4) + TB * PP) * 4, sk = sq + (size_t)TB * PP * 4;
-    cudaFuncSetAttribute(k_dense_dq_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
-    cudaFuncSetAttribute(k_dense_dkv_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_dq_simt<D>, sq, done);
+    }
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_dkv_simt<D>, sk, done);
+    }
     if (a.Nq > 0) {
         ::park::prof_begin(st);
         k_dense_dq_simt<D><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B), 256, sq, st>>>(a, delta);

@@ -693,8 +693,14 @@ __global__ void __launch_bounds__(384, 1)
 template <int NP>
 int bwd_tc(const DenseArgs& a, const CUtensorMap* m, float* delta, float* parts, cudaStream_t st) {
     constexpr size_t sq = bwd_smem<NP, DqSmem>(), sk = bwd_smem<NP, DkvSmem>();
-    cudaFuncSetAttribute(k_dense_dq_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
-    cudaFuncSetAttribute(k_dense_dkv_tc<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sk);
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_dq_tc<NP>, sq, done);
+    }
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_dkv_tc<NP>, sk, done);
+    }
     if (a.Nq > 0) {
         ::park::prof_begin(st);
         k_dense_dq_tc<NP><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, kTile), a.Hq, a.B), 384, sq, st>>>(

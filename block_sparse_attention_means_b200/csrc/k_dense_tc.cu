@@ -478,7 +478,10 @@ template <int NP, int NS>
 int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, const DenseSplit& sp, float* part_o,
            float* part_lse, cudaStream_t st) {
     using C = FwdCfg<NP, NS>;
-    cudaFuncSetAttribute(k_dense_fwd_tc<NP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+    {
+        static std::atomic<uint64_t> done{0};
+        allow_smem(k_dense_fwd_tc<NP, NS>, C::smem, done);
+    }
     const dim3 grid((unsigned)sp.tiles, a.Hk, a.B * sp.n);
     ::park::prof_begin(st);
     k_dense_fwd_tc<NP, NS><<<grid, C::threads, C::smem, st>>>(mK, mV, a, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
