@@ -114,10 +114,11 @@ __device__ __forceinline__ uint8_t* row_ptr(const Op4& o, int b, int h, long lon
     return o.p + (b * o.sb + h * o.sh + n * o.sn) * (long long)sizeof(T);
 }
 
-__device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, int x, int rows, bool by_keys, int rep) {
+__device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, const DenseOrder& o, int x, int rows, bool by_keys,
+                                                 int rep) {
     __shared__ SeqTile sh;
     if (threadIdx.x < 32) {
-        const SeqTile t = dense_resolve(a, x, rows, by_keys, rep);
+        const SeqTile t = dense_block_tile(a, o, x, rows, by_keys, rep);
         if (threadIdx.x == 0) sh = t;
     }
     __syncthreads();
@@ -128,7 +129,7 @@ __device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, int x, int 
 // its keys.  With several parts each writes its normalised o and its log2-sum, joined by k_dense_combine.
 template <int D, int R>
 __global__ void __launch_bounds__(256)
-    k_dense_fwd_simt(DenseArgs a, int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse) {
+    k_dense_fwd_simt(DenseArgs a, DenseOrder order, int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse) {
     constexpr int BM = 16 * R;
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
@@ -136,10 +137,11 @@ __global__ void __launch_bounds__(256)
     float* Vs = Ks + TB * (D + 4);
     float* Ps = Vs + TB * (D + 4);
     const int G = a.Hq / a.Hk;
-    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, BM, false, G);  // causal: long rows first
+    int x;
+    const int bh = dense_block_head(order, x), b = bh / a.Hk, hk = bh - b * a.Hk, sp = blockIdx.z;
+    const SeqTile t = resolve_block(a, order, x, BM, false, G);
     const int r0 = t.tile * BM;
     if (!t.live || r0 >= t.nq * G) return;
-    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(BM, t.nq * G - r0);
     {
@@ -325,17 +327,18 @@ __global__ void __launch_bounds__(256) k_dense_delta(DenseArgs a, float* __restr
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float* __restrict__ delta) {
+__global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta) {
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
     float* Gs = Qs + TB * (D + 4);
     float* Ks = Gs + TB * (D + 4);
     float* Vs = Ks + TB * (D + 4);
     float* Ps = Vs + TB * (D + 4);
-    const SeqTile t = resolve_block(a, gridDim.x - 1 - blockIdx.x, TB, false, 1);
+    int x;
+    const int bh = dense_block_head(order, x), b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
+    const SeqTile t = resolve_block(a, order, x, TB, false, 1);
     const int i0 = t.tile * TB;
     if (!t.live || i0 >= t.nq) return;
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(TB, t.nq - i0);
     load_tile<D, TB>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, const float*
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float* __restrict__ delta, int n_split,
+__global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta, int n_split,
                                                         int chunk, float* __restrict__ part_dv, float* __restrict__ part_dk) {
     extern __shared__ __align__(16) float smem[];
     float* Ks = smem;
@@ -398,10 +401,12 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, const float
     float* Gs = Qs + TB * (D + 4);
     float* Ps = Gs + TB * (D + 4);
     float* Ds = Ps + TB * PP;
-    const SeqTile t = resolve_block(a, blockIdx.x, TB, true, 1);  // causal: the first keys have the most rows
+    int x;
+    const int bh = dense_block_head(order, x), b = bh / a.Hk, hk = bh - b * a.Hk, sp = blockIdx.z;
+    const SeqTile t = resolve_block(a, order, x, TB, true, 1);
     const int j0 = t.tile * TB;
     if (!t.live || j0 >= t.nk) return;
-    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split, G = a.Hq / a.Hk;
+    const int G = a.Hq / a.Hk;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int first, end;
     dense_row_tiles(t, j0, a.causal, TB, first, end);
@@ -514,7 +519,8 @@ int fwd_simt_r(const DenseArgs& a, const DenseSplit& sp, float* part_o, float* p
         allow_smem(k_dense_fwd_simt<D, R>, sm, done);
     }
     ::park::prof_begin(st);
-    k_dense_fwd_simt<D, R><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 256, sm, st>>>(a, sp.n, sp.chunk, part_o, part_lse);
+    k_dense_fwd_simt<D, R><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), 256, sm, st>>>(
+        a, dense_order(a, sp.tiles, a.B * a.Hk, 8 * a.Nk * D, 1), sp.n, sp.chunk, part_o, part_lse);
     PARK_TRY_LAUNCH("k_dense_fwd_simt", st);
     return PARK_OK;
 }
@@ -522,7 +528,7 @@ int fwd_simt_r(const DenseArgs& a, const DenseSplit& sp, float* part_o, float* p
 template <int D>
 int fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st) {
     const DenseSplit sp = dense_split_simt(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
-    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    if (sp.n > 65535) return PARK_ERR_UNSUPPORTED;
     float* part_o = static_cast<float*>(ws);
     float* part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sp.lse_off);
     PARK_CHECK(sp.rows == 128 ? (fwd_simt_r<D, 8>(a, sp, part_o, part_lse, st))
@@ -544,15 +550,18 @@ int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t 
     }
     if (a.Nq > 0) {
         ::park::prof_begin(st);
-        k_dense_dq_simt<D><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, TB), a.Hq, a.B), 256, sq, st>>>(a, delta);
+        const long long tiles = dense_tiles(a.Nq, a.n_seq, TB);
+        k_dense_dq_simt<D><<<(unsigned)(tiles * a.B * a.Hq), 256, sq, st>>>(
+            a, dense_order(a, tiles, a.B * a.Hq, 8 * a.Nk * D, a.Hq / a.Hk), delta);
         PARK_TRY_LAUNCH("k_dense_dq_simt", st);
     }
     if (a.Nk == 0) return PARK_OK;
     const DkvSplit sp = dense_split_dkv(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, D, TB);
-    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    if (sp.n > 65535) return PARK_ERR_UNSUPPORTED;
     float* part_dk = parts + sp.dk_off / 4;
     ::park::prof_begin(st);
-    k_dense_dkv_simt<D><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 256, sk, st>>>(a, delta, sp.n, sp.chunk, parts, part_dk);
+    k_dense_dkv_simt<D><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), 256, sk, st>>>(
+        a, dense_order(a, sp.tiles, a.B * a.Hk, 8 * a.Nq * D * (a.Hq / a.Hk), 1), delta, sp.n, sp.chunk, parts, part_dk);
     PARK_TRY_LAUNCH("k_dense_dkv_simt", st);
     return sp.n > 1 ? launch_dense_dkv_reduce(a, PARK_F32, sp, TB, parts, part_dk, st) : PARK_OK;
 }
@@ -614,16 +623,19 @@ DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int 
 
 // Splits the keys when the row tiles alone leave SMs idle: parts of equal length whatever the sequence (a packed batch
 // holds at most kt key tiles in all, a batch entry has as many), about `waves` CTAs for each SM, at least `least` key
-// tiles each.
-static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long long kt, int n_seq, int D, int waves,
+// tiles each; done when the row tiles are at most `wide` CTAs for two SMs.
+static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long long kt, int n_seq, int D, int waves, int wide,
                        int least) {
     s->n = 1;
     s->chunk = 0;
     const long long work = n_seq > 0 ? kt * Hk : kt * Hk * B * s->tiles;
     long long chunk = (work + (long long)waves * kDenseSMs - 1) / ((long long)waves * kDenseSMs);
+    // long parts in twice as many CTAs (four sequences of 3,601 to 119,056 keys, 24/8 heads: 187 -> 174 us; 8 heads x 30,000
+    // keys would go from 38 to 43)
+    if (chunk >= 32) chunk = (chunk + 1) / 2;
     if (chunk < least) chunk = least;
     const long long n = (kt + chunk - 1) / chunk;
-    if (s->tiles * Hk * B * 2 <= kDenseSMs * (waves > 2 ? 2 : 1) && n > 1) {
+    if (s->tiles * Hk * B * 2 <= kDenseSMs * wide && n > 1) {
         s->n = (int)n;
         s->chunk = (int)chunk;
     }
@@ -640,7 +652,7 @@ DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int
     const long long rows = Nq * (Hq / Hk);
     s.rows = dense_tiles(rows, n_seq, 256) * Hk * B * 2 <= kDenseSMs ? 128 : 256;
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 4);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 1, 4);
     return s;
 }
 
@@ -656,7 +668,7 @@ DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, i
             break;
         }
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2, 2);
     return s;
 }
 

@@ -93,7 +93,7 @@ template <int NP>
 __global__ void __launch_bounds__(384, 1)
     k_dense_dq_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
-                  float* __restrict__ delta, uint64_t wait_ns) {
+                  DenseOrder order, float* __restrict__ delta, uint64_t wait_ns) {
     using C = BwdCfg<NP>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* Qs = smem;
@@ -106,8 +106,10 @@ __global__ void __launch_bounds__(384, 1)
     }
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
+    int x_tile;
+    const int bh = dense_block_head(order, x_tile), b = a.B == 1 ? 0 : bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
     if (warp == 0) {
-        const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, kTile, false, 1);
+        const SeqTile t = dense_block_tile(a, order, x_tile, kTile, false, 1);
         if (lane == 0) {
             sh.seq = t;
             mbar_init(&sh.own_full, 1);
@@ -133,7 +135,6 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const SeqTile t = sh.seq;
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hk);
     const int i0 = t.tile * kTile, rows = t.live ? min(kTile, t.nq - i0) : 0;
     const int kend = rows > 0 ? dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1 : 0;
     const int nt = kend > 0 ? (kend + kTile - 1) / kTile : 0;
@@ -363,7 +364,7 @@ template <int NP>
 __global__ void __launch_bounds__(384, 1)
     k_dense_dkv_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
-                   const float* __restrict__ delta, int n_split, int chunk, float* __restrict__ part_dv,
+                   DenseOrder order, const float* __restrict__ delta, int n_split, int chunk, float* __restrict__ part_dv,
                    float* __restrict__ part_dk, uint64_t wait_ns) {
     using C = BwdCfg<NP>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -377,8 +378,10 @@ __global__ void __launch_bounds__(384, 1)
     }
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
+    int x_tile;
+    const int bh = dense_block_head(order, x_tile), b = a.B == 1 ? 0 : bh / a.Hk, hk = bh - b * a.Hk, sp = blockIdx.z;
     if (warp == 0) {
-        const SeqTile t = dense_resolve(a, blockIdx.x, kTile, true, 1);
+        const SeqTile t = dense_block_tile(a, order, x_tile, kTile, true, 1);
         if (lane == 0) {
             sh.seq = t;
             mbar_init(&sh.own_full, 1);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const SeqTile t = sh.seq;
-    const int hk = blockIdx.y, b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split, G = a.Hq / a.Hk;
+    const int G = a.Hq / a.Hk;
     const int j0 = t.tile * kTile, keys = t.live ? min(kTile, t.nk - j0) : 0;
     // row tiles first .. end-1 of each head of the group see a key of this tile; this part has steps s0 .. s0 + steps - 1
     int first, end;
@@ -702,18 +705,21 @@ int bwd_tc(const DenseArgs& a, const CUtensorMap* m, float* delta, float* parts,
         allow_smem(k_dense_dkv_tc<NP>, sk, done);
     }
     if (a.Nq > 0) {
+        const long long tiles = dense_tiles(a.Nq, a.n_seq, kTile);
+        const DenseOrder order = dense_order(a, tiles, a.B * a.Hq, 4 * a.Nk * a.D, a.Hq / a.Hk);
         ::park::prof_begin(st);
-        k_dense_dq_tc<NP><<<dim3((unsigned)dense_tiles(a.Nq, a.n_seq, kTile), a.Hq, a.B), 384, sq, st>>>(
-            m[0], m[1], m[2], m[3], a, delta, wait_limit_ns());
+        k_dense_dq_tc<NP><<<(unsigned)(tiles * a.B * a.Hq), 384, sq, st>>>(m[0], m[1], m[2], m[3], a, order, delta,
+                                                                           wait_limit_ns());
         PARK_TRY_LAUNCH("k_dense_dq_tc", st);
     }
     if (a.Nk > 0) {
         const DkvSplit sp = dense_split_dkv(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D, kTile);
-        if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+        if (sp.n > 65535) return PARK_ERR_UNSUPPORTED;
         float* part_dk = parts + sp.dk_off / 4;
+        const DenseOrder order = dense_order(a, sp.tiles, a.B * a.Hk, 4 * a.Nq * a.D * (a.Hq / a.Hk), 1);
         ::park::prof_begin(st);
-        k_dense_dkv_tc<NP><<<dim3((unsigned)sp.tiles, a.Hk, a.B * sp.n), 384, sk, st>>>(
-            m[0], m[1], m[2], m[3], a, delta, sp.n, sp.chunk, parts, part_dk, wait_limit_ns());
+        k_dense_dkv_tc<NP><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), 384, sk, st>>>(
+            m[0], m[1], m[2], m[3], a, order, delta, sp.n, sp.chunk, parts, part_dk, wait_limit_ns());
         PARK_TRY_LAUNCH("k_dense_dkv_tc", st);
         if (sp.n > 1) return launch_dense_dkv_reduce(a, PARK_BF16, sp, kTile, parts, part_dk, st);
     }

@@ -123,7 +123,7 @@ __device__ __forceinline__ Piece<NS> fwd_piece(const SeqTile& t, int G, int caus
 template <int NP, int NS>
 __global__ void __launch_bounds__(FwdCfg<NP, NS>::threads, FwdCfg<NP, NS>::ctas)
     k_dense_fwd_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DenseArgs a,
-                   int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse, uint64_t wait_ns) {
+                   DenseOrder order, int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse, uint64_t wait_ns) {
     using C = FwdCfg<NP, NS>;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     __shared__ FwdSmem sh;
@@ -133,8 +133,10 @@ __global__ void __launch_bounds__(FwdCfg<NP, NS>::threads, FwdCfg<NP, NS>::ctas)
     uint8_t* Vs = Ks + C::KS * C::tile;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     volatile int* abort = &sh.abort;
+    int x_tile;
+    const int bh = dense_block_head(order, x_tile), b = a.B == 1 ? 0 : bh / a.Hk, hk = bh - b * a.Hk, sp = blockIdx.z;
     if (warp == 0) {
-        const SeqTile t = dense_resolve(a, gridDim.x - 1 - blockIdx.x, NS * kTile, false, a.Hq / a.Hk);
+        const SeqTile t = dense_block_tile(a, order, x_tile, NS * kTile, false, a.Hq / a.Hk);
         if (lane == 0) {
             sh.seq = t;
             for (int s = 0; s < NS; ++s) {
@@ -167,8 +169,7 @@ __global__ void __launch_bounds__(FwdCfg<NP, NS>::threads, FwdCfg<NP, NS>::ctas)
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const SeqTile t = sh.seq;
-    const int G = a.Hq / a.Hk, hk = blockIdx.y;
-    const int b = blockIdx.z / n_split, sp = blockIdx.z - b * n_split;
+    const int G = a.Hq / a.Hk;
     const Piece<NS> pc = fwd_piece<NS>(t, G, a.causal, n_split, sp, chunk);
     // first key tile (counted within the piece) that some row does not see whole
     const int cut = (dense_last_key(token_of(pc.r0, G), t.nq, t.nk, a.causal) + 1) / kTile - pc.j_lo;
@@ -482,9 +483,10 @@ int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, con
         static std::atomic<uint64_t> done{0};
         allow_smem(k_dense_fwd_tc<NP, NS>, C::smem, done);
     }
-    const dim3 grid((unsigned)sp.tiles, a.Hk, a.B * sp.n);
+    const DenseOrder order = dense_order(a, sp.tiles, a.B * a.Hk, 4 * a.Nk * a.D, 1);
+    const dim3 grid((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n);
     ::park::prof_begin(st);
-    k_dense_fwd_tc<NP, NS><<<grid, C::threads, C::smem, st>>>(mK, mV, a, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
+    k_dense_fwd_tc<NP, NS><<<grid, C::threads, C::smem, st>>>(mK, mV, a, order, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
     PARK_TRY_LAUNCH("k_dense_fwd_tc", st);
     return PARK_OK;
 }
@@ -493,7 +495,7 @@ int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, con
 
 int launch_dense_fwd_tc(const DenseArgs& a, void* ws, cudaStream_t st) {
     const DenseSplit sp = dense_split_tc(a.B, a.Hq, a.Hk, a.Nq, a.Nk, a.n_seq, a.D);
-    if ((long long)a.B * sp.n > 65535) return PARK_ERR_UNSUPPORTED;
+    if (sp.n > 65535) return PARK_ERR_UNSUPPORTED;
     CUtensorMap mK, mV;
     // without keys nothing is loaded; the maps still have to be valid
     PARK_CHECK(map_4d(&mK, a.Nk ? a.k : a.q, a.Nk ? a.B : 1, a.Nk ? a.Hk : 1, a.Nk ? a.Nk : 1, a.D, kTile));
