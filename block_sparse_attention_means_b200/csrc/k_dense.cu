@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder 
             auto see = [&](int r, int c) {
                 return c < rows && r < keys && j0 + r <= dense_last_key(i0 + c, t.nq, t.nk, a.causal);
             };
-            const bool cut = rows < TB || j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
+            const bool cut = rows < TB || j0 + keys - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
             float s[4][4], dp[4][4];
             dot_tile<D, 4>(s, Ks, Qs, ty, tx);
             dot_tile<D, 4>(dp, Vs, Gs, ty, tx);

@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             tc_fence_after();
             // columns lo .. hi of this half are visible to this thread's key
-            const bool cut = i0 + kTile > t.nq || j0 + kTile - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
+            // (keys past the end are lanes of their own, which nothing sums over and nothing writes)
+            const bool cut = i0 + kTile > t.nq || j0 + keys - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
             const int lo = (a.causal ? j0 + row - off - i0 : 0) - 64 * hc, hi = t.nq - 1 - i0 - 64 * hc;
             uint32_t s[2][32];
             ld64(trow + 64 * hc, s);
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(384, 1)
                         for (int g = 0; g < G; ++g)
                             for (int i = first * kTile; i < t.nq; ++i) {
                                 const int ib = i / kTile * kTile;
-                                if (!(ib + kTile > t.nq || j0 + kTile - 1 > dense_last_key(ib, t.nq, t.nk, a.causal)) ||
+                                if (!(ib + kTile > t.nq || j0 + keys - 1 > dense_last_key(ib, t.nq, t.nk, a.causal)) ||
                                     j0 + row > dense_last_key(i, t.nq, t.nk, a.causal))
                                     continue;
                                 const uint16_t* gr = reinterpret_cast<const uint16_t*>(
