@@ -128,7 +128,7 @@ __device__ __forceinline__ SeqTile resolve_block(const DenseArgs& a, const Dense
 // Forward: 16 R rows of a sequence (counted token by token, the heads that share a key head side by side) and a part of
 // its keys.  With several parts each writes its normalised o and its log2-sum, joined by k_dense_combine.
 template <int D, int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, D <= 64 || R == 1 ? 2 : 1)
     k_dense_fwd_simt(DenseArgs a, DenseOrder order, int n_split, int chunk, float* __restrict__ part_o, float* __restrict__ part_lse) {
     constexpr int BM = 16 * R;
     extern __shared__ __align__(16) float smem[];
