@@ -52,10 +52,9 @@ __host__ inline long long dense_tiles(long long n, int n_seq, int tile) {
     return n_seq > 0 ? n / tile + n_seq : (n + tile - 1) / tile;
 }
 
-// Tile x (of `rows` rows, counted along the queries or the keys, a query row
-// counted `rep` times) -> sequence and tile.  Called by one whole warp; packed bounds are read 32
-// sequences at a time.  Bounds that are not 0 <= cu[s] <= cu[s+1] <= N make
-// the sequence empty and set the status word.
+// Tile x (of `rows` rows, counted along the queries, a query row counted `rep` times, or along the keys) -> sequence and
+// tile.  Called by one whole warp; packed bounds are read 128 sequences at a time.  Bounds that are not 0 <= cu[s] <=
+// cu[s+1] <= N make the sequence empty and set the status word.
 __device__ inline SeqTile dense_resolve(const DenseArgs& a, int x, int rows, bool by_keys, int rep) {
     SeqTile t;
     if (a.n_seq == 0) {
@@ -66,39 +65,58 @@ __device__ inline SeqTile dense_resolve(const DenseArgs& a, int x, int rows, boo
         t.live = 1;
         return t;
     }
+    constexpr int U = 4;  // sequences of a lane
     const int lane = threadIdx.x & 31;
     t.q0 = t.nq = t.k0 = t.nk = t.tile = t.live = 0;
     int before = 0;  // tiles of the sequences before this step's
-    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-        const int s = s0 + lane;
-        int qa = 0, qb = 0, ka = 0, kb = 0;
-        if (s < a.n_seq) {
-            qa = a.cu_q[s];
-            qb = a.cu_q[s + 1];
-            ka = a.cu_k[s];
-            kb = a.cu_k[s + 1];
-            if (qa < 0 || qb < qa || qb > a.Nq || ka < 0 || kb < ka || kb > a.Nk) {
-                set_status(a.status, PARK_ERR_INDEX);
-                qb = qa = kb = ka = 0;
-            }
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32 * U) {
+        int q[U + 1], k[U + 1], nt[U], sum = 0;
+        const int first = s0 + lane * U;
+#pragma unroll
+        for (int u = 0; u <= U; ++u) {
+            q[u] = first + u <= a.n_seq ? a.cu_q[first + u] : 0;
+            k[u] = first + u <= a.n_seq ? a.cu_k[first + u] : 0;
         }
-        const long long n = by_keys ? kb - ka : (long long)(qb - qa) * rep;
-        const int nt = (int)((n + rows - 1) / rows);
-        int pre = nt;  // inclusive prefix over the lanes
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            nt[u] = 0;
+            if (first + u < a.n_seq) {
+                if (q[u] < 0 || q[u + 1] < q[u] || q[u + 1] > a.Nq || k[u] < 0 || k[u + 1] < k[u] || k[u + 1] > a.Nk) {
+                    set_status(a.status, PARK_ERR_INDEX);
+                } else {
+                    const long long n = by_keys ? k[u + 1] - k[u] : (long long)(q[u + 1] - q[u]) * rep;
+                    nt[u] = (int)((n + rows - 1) / rows);
+                }
+            }
+            sum += nt[u];
+        }
+        int pre = sum;  // inclusive prefix over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane >= o) pre += v;
         }
-        const int first = before + pre - nt;
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= first && x < first + nt);
+        const int at = before + pre - sum;
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= at && x < at + sum);
         if (hit) {
+            int e = x - at, q0 = 0, q1 = 0, k0 = 0, k1 = 0, tile = -1;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (tile < 0 && e < nt[u]) {
+                    q0 = q[u];
+                    q1 = q[u + 1];
+                    k0 = k[u];
+                    k1 = k[u + 1];
+                    tile = e;
+                }
+                e -= nt[u];
+            }
             const int src = __ffs(hit) - 1;
-            t.q0 = __shfl_sync(0xffffffffu, qa, src);
-            t.nq = __shfl_sync(0xffffffffu, qb, src) - t.q0;
-            t.k0 = __shfl_sync(0xffffffffu, ka, src);
-            t.nk = __shfl_sync(0xffffffffu, kb, src) - t.k0;
-            t.tile = x - __shfl_sync(0xffffffffu, first, src);
+            t.q0 = __shfl_sync(0xffffffffu, q0, src);
+            t.nq = __shfl_sync(0xffffffffu, q1, src) - t.q0;
+            t.k0 = __shfl_sync(0xffffffffu, k0, src);
+            t.nk = __shfl_sync(0xffffffffu, k1, src) - t.k0;
+            t.tile = __shfl_sync(0xffffffffu, tile, src);
             t.live = 1;
             return t;
         }

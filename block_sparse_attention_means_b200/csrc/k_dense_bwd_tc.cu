@@ -655,9 +655,11 @@ __global__ void __launch_bounds__(384, 1)
                         for (int g = 0; g < G; ++g)
                             for (int i = first * kTile; i < t.nq; ++i) {
                                 const int ib = i / kTile * kTile;
-                                if (!(ib + kTile > t.nq || j0 + keys - 1 > dense_last_key(ib, t.nq, t.nk, a.causal)) ||
-                                    j0 + row > dense_last_key(i, t.nq, t.nk, a.causal))
+                                if (!(ib + kTile > t.nq || j0 + keys - 1 > dense_last_key(ib, t.nq, t.nk, a.causal))) {
+                                    i = ib + kTile - 1;  // (not cut)
                                     continue;
+                                }
+                                if (j0 + row > dense_last_key(i, t.nq, t.nk, a.causal)) continue;
                                 const uint16_t* gr = reinterpret_cast<const uint16_t*>(
                                                          a.d_o.p + (b * a.d_o.sb + (hk * G + g) * a.d_o.sh +
                                                                     (t.q0 + (long long)i) * a.d_o.sn) * 2) + d0;

@@ -255,6 +255,8 @@ int park_set_wait_limit_ns(uint64_t ns);
  *   - *status (device, int32[1], not NULL) is written only when a device-side
  *     condition is met and never cleared by these calls: zero it once, read it
  *     whenever convenient; calls may share it.
+ *   - A workspace belongs to one call at a time: calls that may overlap on the GPU
+ *     (other streams, graphs that replay side by side) need one each.
  *   - Outputs may not overlap inputs or one another, except that park_rope,
  *     park_qk_norm_rope and park_qk_norm_rope_bwd may write an output onto an input
  *     of the same side (same pointer and strides). */

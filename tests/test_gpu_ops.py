@@ -446,6 +446,8 @@ PACKED = [
     (6, 2, [1, 1, 2, 1], [700, 3, 129, 1], 96, True, BF, "tokens"),
     (3, 3, [40, 1, 90], [40, 1, 90], 96, True, F32, "tokens"),
     (2, 1, [0, 7, 65], [12, 0, 130], 32, False, F32, "heads"),
+    (2, 1, [1, 0, 2] * 100, [2, 5, 1] * 100, 64, True, BF, "heads"),
+    (2, 1, [3] * 33, [1] * 33, 32, True, F32, "heads"),
     (2, 1, [3] * 70, [4] * 70, 64, True, BF, "heads"),                    # more sequences than a warp scans at once
 ]
 
@@ -668,6 +670,28 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(O, want[0])
     park.attention_bwd(do, q, k, v, *want, causal=True, dQ=O)
     assert torch.equal(O, grads[0])
+
+
+@pytest.mark.parametrize("nq,nk", [(600, 900), (40000, 300)])   # one and two row tiles in a block
+def test_waits_that_run_out_are_reported(nq, nk):
+    """With the wait limit at 1 ns the tensor-core kernels report the timeout and end; the next call is right."""
+    q, k, v, do = attn_inputs(1, 2, 2, nq, nk, 128, BF, "heads")
+    want, lse = park.attention(q, k, v, return_lse=True)
+    grads = park.attention_bwd(do, q, k, v, want, lse)
+    torch.cuda.synchronize()
+    for call in (lambda s: park.attention(q, k, v, status=s),
+                 lambda s: park.attention_bwd(do, q, k, v, want, lse, status=s)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        park.set_wait_limit_ns(1)
+        try:
+            call(status)
+            torch.cuda.synchronize()
+        finally:
+            park.set_wait_limit_ns(0)
+        assert status.item() == _lib.PARK_ERR_TIMEOUT
+        assert torch.equal(park.attention(q, k, v), want)
+        for a, b in zip(park.attention_bwd(do, q, k, v, want, lse), grads):
+            assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------ together
