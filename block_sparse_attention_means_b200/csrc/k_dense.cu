@@ -571,7 +571,7 @@ int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t 
 int launch_dense_combine(const DenseArgs& a, int dtype, int n_split, const float* part_o, const float* part_lse,
                          cudaStream_t st) {
     const long long rows = a.Nq * (a.Hq / a.Hk);
-    const bool wide = n_split > 4;
+    const bool wide = n_split > 4 && rows * a.Hk * a.B <= 2048;
     const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8), a.Hk, a.B);
     ::park::prof_begin(st);
     if (dtype == PARK_BF16) {
@@ -652,23 +652,23 @@ DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int
     const long long rows = Nq * (Hq / Hk);
     s.rows = dense_tiles(rows, n_seq, 256) * Hk * B * 2 <= kDenseSMs ? 128 : 256;
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 1, 4);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 1, 3);
     return s;
 }
 
 DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D) {
-    // the widest row tile that still fills the SMs: 8 rows a thread need half the shared-memory reads of 4, and one row a
-    // thread suits single rows
+    // 8 rows a thread (half the shared-memory reads of 4) where those tiles fill the SMs; one row a thread for single rows, and
+    // for problems so small that a block for each pair of tiles is about one wave; 4 otherwise, with split keys where they do
+    // not fill (1,500 causal rows x 2 heads, D = 64: 114 us with one row, 54 with 4)
     DenseSplit s;
     const long long rows = Nq * (Hq / Hk), mean = n_seq > 0 ? rows / n_seq : rows;
-    s.rows = 16;
-    for (int r : {128, 64})
-        if (mean >= r / 2 && dense_tiles(rows, n_seq, r) * Hk * B >= kDenseSMs) {
-            s.rows = r;
-            break;
-        }
+    const long long kt = (Nk + TB - 1) / TB / (n_seq > 0 ? n_seq : 1) + 1;
+    if (mean >= 64 && dense_tiles(rows, n_seq, 128) * Hk * B >= kDenseSMs)
+        s.rows = 128;
+    else
+        s.rows = mean < 32 || dense_tiles(rows, n_seq, 16) * kt * Hk * B <= 2 * kDenseSMs ? 16 : 64;
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2, 2);
+    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2, 1);
     return s;
 }
 
