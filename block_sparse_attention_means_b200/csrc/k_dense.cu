@@ -38,6 +38,27 @@ __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long l
     }
 }
 
+// The same, asynchronous: one group of copies, rows from n on as zeros.  Nothing is read for n <= 0.
+template <int D>
+__device__ __forceinline__ void fetch_tile(float* dst, const uint8_t* src, long long stride, int n) {
+    constexpr int C = D / 4;
+    const uint32_t d0 = (uint32_t)__cvta_generic_to_shared(dst);
+    for (int i = threadIdx.x; i < TB * C; i += 256) {
+        const int r = i / C, c = i - r * C;
+        const bool on = r < n;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d0 + (r * (D + 4) + 4 * c) * 4),
+                     "l"(on ? src + r * stride * 4 + 16 * c : src), "r"(on ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// The oldest group has landed: all but the newest N groups are waited for.
+template <int N>
+__device__ __forceinline__ void landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncthreads();
+}
+
 // s[i][j] = A[R ty + i] . B[tx + 16 j], even and odd elements in the halves of packed sums
 template <int D, int R>
 __device__ __forceinline__ void dot_tile(float (&s)[R][4], const float* A, const float* Bm, int ty, int tx) {
@@ -174,11 +195,15 @@ __global__ void __launch_bounds__(256, D <= 64 || R == 1 ? 2 : 1)
         j_lo = sp * chunk * TB;
         kend = min(kend, j_lo + chunk * TB);
     }
+    auto key = [&](const Op4& o, int j) { return row_ptr<float>(o, b, hk, t.k0 + min(j, t.nk - 1)); };
+    if (j_lo < kend) {
+        fetch_tile<D>(Ks, key(a.k, j_lo), a.k.sn, t.nk - j_lo);
+        fetch_tile<D>(Vs, key(a.v, j_lo), a.v.sn, t.nk - j_lo);
+    }
     for (int j0 = j_lo; j0 < kend; j0 += TB) {
-        __syncthreads();
-        load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
-        __syncthreads();
+        // K of the next tile is fetched beside P V, V beside the next scores
+        const int jn = j0 + TB, nn = jn < kend ? t.nk - jn : 0;
+        landed<1>();
         const bool cut = j0 + TB - 1 > least;
         float s[R][4];
         dot_tile<D, R>(s, Qs, Ks, ty, tx);
@@ -207,12 +232,17 @@ __global__ void __launch_bounds__(256, D <= 64 || R == 1 ? 2 : 1)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) acc[i][c] = __fmul2_rn(acc[i][c], make_float2(alpha, alpha));
         }
-        __syncwarp();  // (a row's probabilities come from its own half-warp)
+        __syncthreads();
+        fetch_tile<D>(Ks, key(a.k, jn), a.k.sn, nn);
+        landed<1>();
         if (cut)
             accumulate<D, R, true>(acc, Ps, Vs, ty, tx, [&](int r, int c) { return j0 + c <= last[r - R * ty]; });
         else
             accumulate<D, R, false>(acc, Ps, Vs, ty, tx, [](int, int) { return true; });
+        __syncthreads();
+        fetch_tile<D>(Vs, key(a.v, jn), a.v.sn, nn);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     const size_t rows_all = (size_t)a.B * a.Hq * a.Nq;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -332,7 +362,7 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder o
     float* Qs = smem;
     float* Gs = Qs + TB * (D + 4);
     float* Ks = Gs + TB * (D + 4);
-    float* Vs = Ks + TB * (D + 4);
+    float* Vs = Ks + 2 * TB * (D + 4);  // (K twice)
     float* Ps = Vs + TB * (D + 4);
     int x;
     const int bh = dense_block_head(order, x), b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
@@ -356,15 +386,21 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder o
     }
     const float sl2 = a.scale * kLog2e;
     const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;
+    auto key = [&](const Op4& o, int j) { return row_ptr<float>(o, b, hk, t.k0 + min(j, t.nk - 1)); };
+    if (kend > 0) {
+        fetch_tile<D>(Ks, key(a.k, 0), a.k.sn, t.nk);
+        fetch_tile<D>(Vs, key(a.v, 0), a.v.sn, t.nk);
+    }
+    float *Kj = Ks, *Kn = Ks + TB * (D + 4);
     for (int j0 = 0; j0 < kend; j0 += TB) {
-        __syncthreads();
-        load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, min(TB, t.nk - j0));
-        load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, min(TB, t.nk - j0));
-        __syncthreads();
+        const int jn = j0 + TB, nn = jn < kend ? t.nk - jn : 0;
+        landed<1>();
+        fetch_tile<D>(Kn, key(a.k, jn), a.k.sn, nn);
         auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
         const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
         float s[4][4], dp[4][4];
-        dot_tile<D, 4>(s, Qs, Ks, ty, tx);
+        dot_tile<D, 4>(s, Qs, Kj, ty, tx);
+        landed<1>();
         dot_tile<D, 4>(dp, Gs, Vs, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -375,11 +411,16 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder o
                 Ps[(4 * ty + i) * PP + tx + 16 * j] = ds;
             }
         __syncthreads();
+        fetch_tile<D>(Vs, key(a.v, jn), a.v.sn, nn);
         if (cut)
-            accumulate<D, 4, true>(acc, Ps, Ks, ty, tx, see);
+            accumulate<D, 4, true>(acc, Ps, Kj, ty, tx, see);
         else
-            accumulate<D, 4, false>(acc, Ps, Ks, ty, tx, see);
+            accumulate<D, 4, false>(acc, Ps, Kj, ty, tx, see);
+        float* swap = Kj;
+        Kj = Kn;
+        Kn = swap;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
@@ -423,13 +464,18 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder 
         for (int c = 0; c < D / 32; ++c) dk[i][c] = dv[i][c] = make_float2(0.f, 0.f);
     const float sl2 = a.scale * kLog2e;
     {
+        auto fetch = [&](float* dst, const Op4& o, int step) {  // (steps past the last one fetch nothing)
+            const int st = min(step, s1 - 1), i = (first + st % per) * TB;
+            fetch_tile<D>(dst, row_ptr<float>(o, b, hk * G + st / per, t.q0 + i), o.sn, step < s1 ? t.nq - i : 0);
+        };
+        if (s0 < s1) {
+            fetch(Qs, a.q, s0);
+            fetch(Gs, a.d_o, s0);
+        }
         for (int step = s0; step < s1; ++step) {
             const int h = hk * G + step / per, i0 = (first + step % per) * TB;
             const int rows = min(TB, t.nq - i0);
-            __syncthreads();
-            load_tile<D, TB>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-            load_tile<D, TB>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
-            __syncthreads();
+            landed<1>();
             // r: key of the tile, c: query row of the tile
             auto see = [&](int r, int c) {
                 return c < rows && r < keys && j0 + r <= dense_last_key(i0 + c, t.nq, t.nk, a.causal);
@@ -437,6 +483,7 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder 
             const bool cut = rows < TB || j0 + keys - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
             float s[4][4], dp[4][4];
             dot_tile<D, 4>(s, Ks, Qs, ty, tx);
+            landed<0>();
             dot_tile<D, 4>(dp, Vs, Gs, ty, tx);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -452,15 +499,22 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder 
                     Ds[(4 * ty + i) * PP + c] = ds;
                 }
             }
-            __syncthreads();
-            if (cut) {
-                accumulate<D, 4, true>(dv, Ps, Gs, ty, tx, see);
+            __syncwarp();  // (a row of p and ds comes from its own half-warp)
+            // Q of the next step is fetched beside dv, dO beside the next scores
+            if (cut)
                 accumulate<D, 4, true>(dk, Ds, Qs, ty, tx, see);
-            } else {
-                accumulate<D, 4, false>(dv, Ps, Gs, ty, tx, see);
+            else
                 accumulate<D, 4, false>(dk, Ds, Qs, ty, tx, see);
-            }
+            __syncthreads();
+            fetch(Qs, a.q, step + 1);
+            if (cut)
+                accumulate<D, 4, true>(dv, Ps, Gs, ty, tx, see);
+            else
+                accumulate<D, 4, false>(dv, Ps, Gs, ty, tx, see);
+            __syncthreads();
+            fetch(Gs, a.d_o, step + 1);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -539,7 +593,7 @@ int fwd_simt(const DenseArgs& a, void* ws, cudaStream_t st) {
 
 template <int D>
 int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t st) {
-    const size_t sq = (size_t)(4 * TB * (D + 4) + TB * PP) * 4, sk = sq + (size_t)TB * PP * 4;
+    const size_t sq = (size_t)(5 * TB * (D + 4) + TB * PP) * 4, sk = (size_t)(4 * TB * (D + 4) + 2 * TB * PP) * 4;
     {
         static std::atomic<uint64_t> done{0};
         allow_smem(k_dense_dq_simt<D>, sq, done);
@@ -605,9 +659,11 @@ DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int 
     s.n = 1;
     s.chunk = 0;
     const long long G = Hq / Hk, steps = (Nq + tile - 1) / tile * G, ctas = s.tiles * Hk * B;
-    if (ctas * 2 <= kDenseSMs) {
+    // (float32 steps are ten times as long, and up to four blocks for an SM are split too)
+    const int waves = tile == 64 ? 4 : 2;
+    if (ctas * 2 <= kDenseSMs * (tile == 64 ? 8 : 1)) {
         const long long work = n_seq > 0 ? (steps + n_seq * G) * ((s.tiles + n_seq - 1) / n_seq) * Hk : steps * ctas;
-        long long chunk = (work + 2 * kDenseSMs - 1) / (2 * kDenseSMs);
+        long long chunk = (work + waves * kDenseSMs - 1) / (waves * kDenseSMs);
         if (chunk < 8) chunk = 8;
         const long long n = (steps + chunk - 1) / chunk;  // (a sequence has at most all the steps)
         if (n > 1) {
