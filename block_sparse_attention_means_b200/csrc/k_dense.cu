@@ -9,9 +9,11 @@
 //   p = exp(s - lse),  ds = p (do v^T - delta),  dq = scale ds k,
 //   dk = scale ds^T q,  dv = p^T do
 //
-// Bound by the FMA units: 64 x 64 score tiles, 256 threads with 4 x 4 scores and
-// 4 x D/16 outputs each; tiles stay in shared memory (row pitch D + 4 floats: the
-// 16 key rows that a half-warp reads with 16-byte loads hit all banks once).
+// Bound by the FMA units and the shared-memory reads that feed them: tiles of 64 keys,
+// R x 4 scores and R x D/16 outputs a thread (R = 8, 4 or 1 rows; 4 in the backward
+// kernels), products in packed pairs; tiles stay in shared memory (row pitch D + 4
+// floats: the 16 key rows that a half-warp reads with 16-byte loads hit all banks
+// once) and the next ones are fetched beside the arithmetic.
 // Tiles that a mask cuts take a variant whose products skip the hidden pairs, so
 // that an infinity or NaN there stays out of the sums.
 #include "dense.cuh"
@@ -27,10 +29,10 @@ __device__ __forceinline__ float4 load4(const uint8_t* p, int i) {
     return *reinterpret_cast<const float4*>(p + 16 * (size_t)i);
 }
 // rows 0 .. n-1 of `src` (row stride in elements) into a [ROWS][D + 4] tile, zeros below
-template <int D, int ROWS>
+template <int D, int ROWS, int NT = 256>
 __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long long stride, int n) {
     constexpr int C = D / 4;
-    for (int i = threadIdx.x; i < ROWS * C; i += 256) {
+    for (int i = threadIdx.x; i < ROWS * C; i += NT) {
         const int r = i / C, c = i - r * C;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n) v = load4(src + r * stride * 4, c);
@@ -39,11 +41,11 @@ __device__ __forceinline__ void load_tile(float* dst, const uint8_t* src, long l
 }
 
 // The same, asynchronous: one group of copies, rows from n on as zeros.  Nothing is read for n <= 0.
-template <int D>
+template <int D, int NT = 256>
 __device__ __forceinline__ void fetch_tile(float* dst, const uint8_t* src, long long stride, int n) {
     constexpr int C = D / 4;
     const uint32_t d0 = (uint32_t)__cvta_generic_to_shared(dst);
-    for (int i = threadIdx.x; i < TB * C; i += 256) {
+    for (int i = threadIdx.x; i < TB * C; i += NT) {
         const int r = i / C, c = i - r * C;
         const bool on = r < n;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d0 + (r * (D + 4) + 4 * c) * 4),
@@ -91,9 +93,9 @@ __device__ __forceinline__ void dot_tile(float (&s)[R][4], const float* A, const
 // acc[i][c] += sum_k P[R ty + i][k] B[k][cols 2 tx + 32 c, + 1].  With MASK only pairs that see(row, k) allows enter.
 template <int D, int R, bool MASK, typename F>
 __device__ __forceinline__ void accumulate(float2 (&acc)[R][D / 32], const float* P, const float* Bm, int ty, int tx,
-                                           F see) {
+                                           F see, int k0 = 0, int k1 = TB) {
 #pragma unroll 1
-    for (int k = 0; k < TB; k += 4) {
+    for (int k = k0; k < k1; k += 4) {
         float4 p[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(P + (R * ty + i) * PP + k);
@@ -356,8 +358,14 @@ __global__ void __launch_bounds__(256) k_dense_delta(DenseArgs a, float* __restr
     }
 }
 
+// In the two backward kernels 256 threads form the scores and 256 others do v^T: one block fills the shared memory of an SM,
+// and eight warps left the FMA units idle.  dq and dk/dv, 32 query heads on 8, 1,145 tokens: D = 128 865 and 1,258 us with
+// 256 threads that did both, 887 and 1,182 with 512; D = 64 501 and 745, 476 and 674.  Halves of 128 threads with 8 x 4
+// elements each, for fewer shared-memory reads: 957 and 1,229.
+constexpr int kBwdThreads = 512;
+
 template <int D>
-__global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta) {
+__global__ void __launch_bounds__(kBwdThreads) k_dense_dq_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta) {
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
     float* Gs = Qs + TB * (D + 4);
@@ -369,62 +377,84 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder o
     const SeqTile t = resolve_block(a, order, x, TB, false, 1);
     const int i0 = t.tile * TB;
     if (!t.live || i0 >= t.nq) return;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = (tid >> 4) & 15;
+    const bool second = tid >= 256;
     const int rows = min(TB, t.nq - i0);
-    load_tile<D, TB>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
-    load_tile<D, TB>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
+    load_tile<D, TB, kBwdThreads>(Qs, row_ptr<float>(a.q, b, h, t.q0 + i0), a.q.sn, rows);
+    load_tile<D, TB, kBwdThreads>(Gs, row_ptr<float>(a.d_o, b, h, t.q0 + i0), a.d_o.sn, rows);
     float2 acc[4][D / 32];
-    float lse2[4], del[4];
+    float stat[4];  // of the rows 4 ty ..: lse in base 2, or delta in the second half
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         const size_t at = ((size_t)b * a.Hq + h) * a.Nq + t.q0 + i0 + r;
-        lse2[i] = r < rows ? a.lse[at] * kLog2e : 0.f;
-        del[i] = r < rows ? delta[at] : 0.f;
+        stat[i] = r < rows ? (second ? delta[at] : a.lse[at] * kLog2e) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
-    }
     const float sl2 = a.scale * kLog2e;
     const int kend = dense_last_key(i0 + rows - 1, t.nq, t.nk, a.causal) + 1;
     auto key = [&](const Op4& o, int j) { return row_ptr<float>(o, b, hk, t.k0 + min(j, t.nk - 1)); };
     if (kend > 0) {
-        fetch_tile<D>(Ks, key(a.k, 0), a.k.sn, t.nk);
-        fetch_tile<D>(Vs, key(a.v, 0), a.v.sn, t.nk);
+        fetch_tile<D, kBwdThreads>(Ks, key(a.k, 0), a.k.sn, t.nk);
+        fetch_tile<D, kBwdThreads>(Vs, key(a.v, 0), a.v.sn, t.nk);
     }
     float *Kj = Ks, *Kn = Ks + TB * (D + 4);
     for (int j0 = 0; j0 < kend; j0 += TB) {
         const int jn = j0 + TB, nn = jn < kend ? t.nk - jn : 0;
-        landed<1>();
-        fetch_tile<D>(Kn, key(a.k, jn), a.k.sn, nn);
+        landed<0>();
+        fetch_tile<D, kBwdThreads>(Kn, key(a.k, jn), a.k.sn, nn);
         auto see = [&](int r, int c) { return j0 + c <= dense_last_key(i0 + r, t.nq, t.nk, a.causal); };
         const bool cut = j0 + TB - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
-        float s[4][4], dp[4][4];
-        dot_tile<D, 4>(s, Qs, Kj, ty, tx);
-        landed<1>();
-        dot_tile<D, 4>(dp, Gs, Vs, ty, tx);
+        float s[4][4];
+        dot_tile<D, 4>(s, second ? Gs : Qs, second ? Vs : Kj, ty, tx);
+        if (!second) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float ds = exp2f(s[i][j] * sl2 - lse2[i]) * (dp[i][j] - del[i]);
-                if (cut && !see(4 * ty + i, tx + 16 * j)) ds = 0.f;
-                Ps[(4 * ty + i) * PP + tx + 16 * j] = ds;
-            }
+                for (int j = 0; j < 4; ++j) Ps[(4 * ty + i) * PP + tx + 16 * j] = exp2f(s[i][j] * sl2 - stat[i]);
+        }
         __syncthreads();
-        fetch_tile<D>(Vs, key(a.v, jn), a.v.sn, nn);
+        fetch_tile<D, kBwdThreads>(Vs, key(a.v, jn), a.v.sn, nn);
+        if (second) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float* at = Ps + (4 * ty + i) * PP + tx + 16 * j;
+                    *at = cut && !see(4 * ty + i, tx + 16 * j) ? 0.f : *at * (s[i][j] - stat[i]);
+                }
+        }
+        __syncthreads();
+        // each half sums over half of the keys
+        const int k0 = second ? TB / 2 : 0;
         if (cut)
-            accumulate<D, 4, true>(acc, Ps, Kj, ty, tx, see);
+            accumulate<D, 4, true>(acc, Ps, Kj, ty, tx, see, k0, k0 + TB / 2);
         else
-            accumulate<D, 4, false>(acc, Ps, Kj, ty, tx, see);
+            accumulate<D, 4, false>(acc, Ps, Kj, ty, tx, see, k0, k0 + TB / 2);
         float* swap = Kj;
         Kj = Kn;
         Kn = swap;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    landed<0>();
+    float* sum = Qs;  // the second half's sums
+    if (second) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<float2*>(sum + (4 * ty + i) * (D + 4) + 2 * tx + 32 * c) = acc[i][c];
+    }
+    __syncthreads();
+    if (second) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= rows) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            acc[i][c] = __fadd2_rn(acc[i][c], *reinterpret_cast<const float2*>(sum + r * (D + 4) + 2 * tx + 32 * c));
         uint8_t* row = row_ptr<float>(a.dq, b, h, t.q0 + i0 + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
@@ -432,9 +462,12 @@ __global__ void __launch_bounds__(256) k_dense_dq_simt(DenseArgs a, DenseOrder o
     }
 }
 
+// The first half of the threads goes on with dv, the second with dk.  The next step's rows travel through registers while
+// these sums are formed (two more tiles do not fit in shared memory at D = 128).
 template <int D>
-__global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta, int n_split,
-                                                        int chunk, float* __restrict__ part_dv, float* __restrict__ part_dk) {
+__global__ void __launch_bounds__(kBwdThreads) k_dense_dkv_simt(DenseArgs a, DenseOrder order, const float* __restrict__ delta,
+                                                                int n_split, int chunk, float* __restrict__ part_dv,
+                                                                float* __restrict__ part_dk) {
     extern __shared__ __align__(16) float smem[];
     float* Ks = smem;
     float* Vs = Ks + TB * (D + 4);
@@ -448,93 +481,106 @@ __global__ void __launch_bounds__(256) k_dense_dkv_simt(DenseArgs a, DenseOrder 
     const int j0 = t.tile * TB;
     if (!t.live || j0 >= t.nk) return;
     const int G = a.Hq / a.Hk;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = (tid >> 4) & 15;
+    const bool second = tid >= 256;
     int first, end;
     dense_row_tiles(t, j0, a.causal, TB, first, end);
     const int per = end - first, s0 = n_split > 1 ? sp * chunk : 0;
     const int s1 = n_split > 1 ? min(per * G, s0 + chunk) : per * G;
     if (n_split > 1 && s0 >= s1) return;  // (no such part)
     const int keys = min(TB, t.nk - j0);
-    load_tile<D, TB>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
-    load_tile<D, TB>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
-    float2 dk[4][D / 32], dv[4][D / 32];
+    load_tile<D, TB, kBwdThreads>(Ks, row_ptr<float>(a.k, b, hk, t.k0 + j0), a.k.sn, keys);
+    load_tile<D, TB, kBwdThreads>(Vs, row_ptr<float>(a.v, b, hk, t.k0 + j0), a.v.sn, keys);
+    float2 acc[4][D / 32];  // dv or dk
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) dk[i][c] = dv[i][c] = make_float2(0.f, 0.f);
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
     const float sl2 = a.scale * kLog2e;
-    {
-        auto fetch = [&](float* dst, const Op4& o, int step) {  // (steps past the last one fetch nothing)
-            const int st = min(step, s1 - 1), i = (first + st % per) * TB;
-            fetch_tile<D>(dst, row_ptr<float>(o, b, hk * G + st / per, t.q0 + i), o.sn, step < s1 ? t.nq - i : 0);
-        };
-        if (s0 < s1) {
-            fetch(Qs, a.q, s0);
-            fetch(Gs, a.d_o, s0);
-        }
-        for (int step = s0; step < s1; ++step) {
-            const int h = hk * G + step / per, i0 = (first + step % per) * TB;
-            const int rows = min(TB, t.nq - i0);
-            landed<1>();
-            // r: key of the tile, c: query row of the tile
-            auto see = [&](int r, int c) {
-                return c < rows && r < keys && j0 + r <= dense_last_key(i0 + c, t.nq, t.nk, a.causal);
-            };
-            const bool cut = rows < TB || j0 + keys - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
-            float s[4][4], dp[4][4];
-            dot_tile<D, 4>(s, Ks, Qs, ty, tx);
-            landed<0>();
-            dot_tile<D, 4>(dp, Vs, Gs, ty, tx);
+    constexpr int F = TB * D / 4 / kBwdThreads;  // 16-byte pieces of a tile for each thread
+    float4 qn[F], gn[F];
+    float stat[4];  // of the columns tx + 16 j: lse in base 2, or delta in the second half
+    auto fetch = [&](int step) {  // the step's rows and statistics into registers
+        const int h = hk * G + step / per, i0 = (first + step % per) * TB, rows = t.nq - i0;
+        const uint8_t *qp = row_ptr<float>(a.q, b, h, t.q0 + i0), *gp = row_ptr<float>(a.d_o, b, h, t.q0 + i0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = tx + 16 * j;
-                const size_t at = ((size_t)b * a.Hq + h) * a.Nq + t.q0 + i0 + c;
-                const float lse2 = c < rows ? a.lse[at] * kLog2e : 0.f, del = c < rows ? delta[at] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p = exp2f(s[i][j] * sl2 - lse2);
-                    float ds = p * (dp[i][j] - del);
-                    if (cut && !see(4 * ty + i, c)) p = ds = 0.f;
-                    Ps[(4 * ty + i) * PP + c] = p;
-                    Ds[(4 * ty + i) * PP + c] = ds;
-                }
+        for (int f = 0; f < F; ++f) {
+            const int i = tid + kBwdThreads * f, r = i / (D / 4), c = i - r * (D / 4);
+            qn[f] = gn[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                qn[f] = load4(qp + r * a.q.sn * 4, c);
+                gn[f] = load4(gp + r * a.d_o.sn * 4, c);
             }
-            __syncwarp();  // (a row of p and ds comes from its own half-warp)
-            // Q of the next step is fetched beside dv, dO beside the next scores
-            if (cut)
-                accumulate<D, 4, true>(dk, Ds, Qs, ty, tx, see);
-            else
-                accumulate<D, 4, false>(dk, Ds, Qs, ty, tx, see);
-            __syncthreads();
-            fetch(Qs, a.q, step + 1);
-            if (cut)
-                accumulate<D, 4, true>(dv, Ps, Gs, ty, tx, see);
-            else
-                accumulate<D, 4, false>(dv, Ps, Gs, ty, tx, see);
-            __syncthreads();
-            fetch(Gs, a.d_o, step + 1);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = tx + 16 * j;
+            const size_t at = ((size_t)b * a.Hq + h) * a.Nq + t.q0 + i0 + c;
+            stat[j] = c < rows ? (second ? delta[at] : a.lse[at] * kLog2e) : 0.f;
+        }
+    };
+    auto keep = [&]() {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int i = tid + kBwdThreads * f, r = i / (D / 4), c = i - r * (D / 4);
+            *reinterpret_cast<float4*>(Qs + r * (D + 4) + 4 * c) = qn[f];
+            *reinterpret_cast<float4*>(Gs + r * (D + 4) + 4 * c) = gn[f];
+        }
+        __syncthreads();
+    };
+    if (s0 < s1) {
+        fetch(s0);
+        keep();
     }
+    for (int step = s0; step < s1; ++step) {
+        const int i0 = (first + step % per) * TB, rows = min(TB, t.nq - i0);
+        // r: key of the tile, c: query row of the tile
+        auto see = [&](int r, int c) {
+            return c < rows && r < keys && j0 + r <= dense_last_key(i0 + c, t.nq, t.nk, a.causal);
+        };
+        const bool cut = rows < TB || j0 + keys - 1 > dense_last_key(i0, t.nq, t.nk, a.causal);
+        float s[4][4];
+        dot_tile<D, 4>(s, second ? Vs : Ks, second ? Gs : Qs, ty, tx);
+        if (!second) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * ty + i, c = tx + 16 * j;
+                    const float p = exp2f(s[i][j] * sl2 - stat[j]);
+                    Ps[r * PP + c] = cut && !see(r, c) ? 0.f : p;
+                }
+        }
+        __syncthreads();
+        if (second) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * ty + i, c = tx + 16 * j;
+                    Ds[r * PP + c] = cut && !see(r, c) ? 0.f : Ps[r * PP + c] * (s[i][j] - stat[j]);
+                }
+            __syncwarp();  // (a row of ds comes from its own half-warp)
+        }
+        if (step + 1 < s1) fetch(step + 1);
+        if (cut)
+            accumulate<D, 4, true>(acc, second ? Ds : Ps, second ? Qs : Gs, ty, tx, see);
+        else
+            accumulate<D, 4, false>(acc, second ? Ds : Ps, second ? Qs : Gs, ty, tx, see);
+        __syncthreads();
+        if (step + 1 < s1) keep();
+    }
+    const Op4& out = second ? a.dk : a.dv;
+    float* part = second ? part_dk : part_dv;
+    const float f = second && n_split == 1 ? a.scale : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= keys) continue;
-        uint8_t *rk, *rv;
-        if (n_split > 1) {
-            const size_t at = (((size_t)sp * a.B + b) * a.Hk + hk) * a.Nk + t.k0 + j0 + r;
-            rk = reinterpret_cast<uint8_t*>(part_dk + at * D);
-            rv = reinterpret_cast<uint8_t*>(part_dv + at * D);
-        } else {
-            rk = row_ptr<float>(a.dk, b, hk, t.k0 + j0 + r);
-            rv = row_ptr<float>(a.dv, b, hk, t.k0 + j0 + r);
-        }
-        const float f = n_split > 1 ? 1.f : a.scale;
+        uint8_t* row = n_split > 1 ? reinterpret_cast<uint8_t*>(part + ((((size_t)sp * a.B + b) * a.Hk + hk) * a.Nk + t.k0 + j0 + r) * D)
+                                   : row_ptr<float>(out, b, hk, t.k0 + j0 + r);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            store2(rk, 2 * tx + 32 * c, dk[i][c].x * f, dk[i][c].y * f);
-            store2(rv, 2 * tx + 32 * c, dv[i][c].x, dv[i][c].y);
-        }
+        for (int c = 0; c < D / 32; ++c) store2(row, 2 * tx + 32 * c, acc[i][c].x * f, acc[i][c].y * f);
     }
 }
 
@@ -605,7 +651,7 @@ int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t 
     if (a.Nq > 0) {
         ::park::prof_begin(st);
         const long long tiles = dense_tiles(a.Nq, a.n_seq, TB);
-        k_dense_dq_simt<D><<<(unsigned)(tiles * a.B * a.Hq), 256, sq, st>>>(
+        k_dense_dq_simt<D><<<(unsigned)(tiles * a.B * a.Hq), kBwdThreads, sq, st>>>(
             a, dense_order(a, tiles, a.B * a.Hq, 8 * a.Nk * D, a.Hq / a.Hk), delta);
         PARK_TRY_LAUNCH("k_dense_dq_simt", st);
     }
@@ -614,7 +660,7 @@ int bwd_simt(const DenseArgs& a, const float* delta, float* parts, cudaStream_t 
     if (sp.n > 65535) return PARK_ERR_UNSUPPORTED;
     float* part_dk = parts + sp.dk_off / 4;
     ::park::prof_begin(st);
-    k_dense_dkv_simt<D><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), 256, sk, st>>>(
+    k_dense_dkv_simt<D><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), kBwdThreads, sk, st>>>(
         a, dense_order(a, sp.tiles, a.B * a.Hk, 8 * a.Nq * D * (a.Hq / a.Hk), 1), delta, sp.n, sp.chunk, parts, part_dk);
     PARK_TRY_LAUNCH("k_dense_dkv_simt", st);
     return sp.n > 1 ? launch_dense_dkv_reduce(a, PARK_F32, sp, TB, parts, part_dk, st) : PARK_OK;
