@@ -461,8 +461,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kBwdBlocks)
         const float2 sums = row_sum<LPR>(make_float2(dot(xx, xx), dot(gx, w)));  // sum x^2, sum h x
         const float r = rsqrtf(sums.x * inv_d + eps);
         dw = fma(gx, r, dw);  // (rows past the end hold zeros)
-        // dx = r (g w - x r mean(h xh)), mean(h xh) = r sum(h x) / D
-        const Quad dx = fma(g, mul(w, r), mul(xx, -r * r * r * sums.y * inv_d));
+        // dx = r (g w - x r mean(h xh)), mean(h xh) = r sum(h x) / D; the mean first: r^3 alone leaves float32's range at rows
+        // of 1e13
+        const float mean = sums.y * r * inv_d;
+        const Quad dx = fma(g, mul(w, r), mul(xx, -mean * r * r));
         if (on) store_quad<HALF>(dx, at_y, l, D, T{});
         left_at -= RPW;
         at_y += RPW * yh;

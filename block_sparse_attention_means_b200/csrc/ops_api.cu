@@ -75,6 +75,8 @@ bool weights_ok(const void* w, int wdtype) {
            reinterpret_cast<uintptr_t>(w) % (wdtype == PARK_BF16 ? 2 : 4) == 0;
 }
 
+bool eps_ok(float eps) { return eps >= 0x1p-80f && std::isfinite(eps); }  // (the gradient forms 1 / eps)
+
 int sm_count() {
     int dev = 0, n = 148;
     if (cudaGetDevice(&dev) == cudaSuccess &&
@@ -183,7 +185,7 @@ int park_qk_norm_rope(const park_operand* q, const park_operand* k, const void* 
                       int32_t* status, void* stream) {
     PARK_CHECK(check_head_dim(D, dtype));
     PARK_CHECK(check_tokens(B, N, rope, positions, pos_sb, D, status));
-    if (!(eps > 0.f) || !std::isfinite(eps) || !weights_ok(wq, wdtype) || !weights_ok(wk, wdtype))
+    if (!eps_ok(eps) || !weights_ok(wq, wdtype) || !weights_ok(wk, wdtype))
         return PARK_ERR_INVALID_ARG;
     const int elt = dtype == PARK_BF16 ? 2 : 4;
     for (const park_operand* op : {q, k}) PARK_CHECK(check_operand(op, B, N, D, elt, false));
@@ -208,7 +210,7 @@ int park_qk_norm_rope_bwd(const park_operand* dq_out, const park_operand* dk_out
                           int D, int dtype, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
     PARK_CHECK(check_head_dim(D, dtype));
     PARK_CHECK(check_tokens(B, N, rope, positions, pos_sb, D, status));
-    if (!(eps > 0.f) || !std::isfinite(eps) || !weights_ok(wq, wdtype) || !weights_ok(wk, wdtype))
+    if (!eps_ok(eps) || !weights_ok(wq, wdtype) || !weights_ok(wk, wdtype))
         return PARK_ERR_INVALID_ARG;
     const int elt = dtype == PARK_BF16 ? 2 : 4;
     for (const park_operand* op : {dq_out, dk_out, q, k}) PARK_CHECK(check_operand(op, B, N, D, elt, false));

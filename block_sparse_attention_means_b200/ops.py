@@ -286,7 +286,7 @@ def _contiguous_like(t):
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope: Rope | None = None, positions=None, eps: float = 1e-6,
                  q_out=None, k_out=None, status=None, stream=None):
-    """(q', k'): each head row divided by its root mean square (with eps > 0), times the
+    """(q', k'): each head row divided by its root mean square (with eps, at least 2^-80), times the
     weight [D] (None: ones), rotated as by ``rope`` (None: not), in one pass, float32
     inside and rounded once.  q has H heads, k may have fewer.  New outputs are
     contiguous [B, H, N, D], the layout that layer() takes; q_out may be q, k_out k."""

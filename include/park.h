@@ -302,7 +302,7 @@ int park_rope(const park_operand *x, const park_operand *y, int B, int64_t N, in
 
 /* For each head row of Q and K: y = R(w x / sqrt(mean x^2 + eps)), computed in
  * float32 and rounded once.  wq, wk: [D] in wdtype (PARK_BF16 or PARK_F32), NULL =
- * all ones.  rope NULL: no rotation (positions must then be NULL).  eps > 0. */
+ * all ones.  rope NULL: no rotation (positions must then be NULL).  eps >= 2^-80. */
 int park_qk_norm_rope(const park_operand *q, const park_operand *k, const void *wq, const void *wk, int wdtype,
                       float eps, const park_rope_axes *rope, const int32_t *positions, int64_t pos_sb,
                       const park_operand *q_out, const park_operand *k_out, int B, int64_t N, int D, int dtype,

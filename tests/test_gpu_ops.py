@@ -287,6 +287,25 @@ def test_norm_rope_gradient_against_differences():
         assert abs(got - slope) <= 1e-5 * (grads[i].double() * d).abs().sum()
 
 
+@pytest.mark.parametrize("size,eps", [(1e17, 1e-6), (1e14, 1e-6), (1e-14, 1e-24), (0.0, 1e-24)])
+def test_norm_rope_rows_of_any_size(size, eps):
+    """Rows whose 1/rms has a cube, or a square times the sums, out of float32's range; bounds as above."""
+    D = 64
+    q, k = rand(62, 1, 3, 9, D) * size, rand(63, 1, 1, 9, D) * size
+    gq, gk, w = rand(64, 1, 3, 9, D), rand(65, 1, 1, 9, D), 1 + 0.3 * rand(66, D)
+    out = park.qk_norm_rope(q, k, w, w, eps=eps)
+    dq, dk, dwq, dwk = park.qk_norm_rope_bwd(gq, gk, q, k, w, w, eps=eps)
+    for y, got, dw, x, gy in ((out[0], dq, dwq, q, gq), (out[1], dk, dwk, k, gk)):
+        x64, wd, g = x.double(), w.double(), gy.double()
+        rr = ((x64 ** 2).mean(-1, keepdim=True) + eps).rsqrt()
+        within(y, x64 * rr * wd, (U[F32] + 16 * E) * (x64 * rr * wd).abs())
+        h, xh = g * wd, x64 * rr
+        want = rr * (h - xh * (h * xh).mean(-1, keepdim=True))
+        mean_abs = (h * xh).abs().mean(-1, keepdim=True)
+        within(got, want, U[F32] * want.abs() + rr * E * (24 * h.abs() + 48 * xh.abs() * mean_abs))
+        within(dw, (g * xh).sum((0, 1, 2)), (27 + 118) * E * (g * xh).abs().sum((0, 1, 2)))
+
+
 def test_norm_rope_same_bits_and_in_place():
     n, q, k, w, r, c, s = norm_inputs(2, 5, 3, (3, 7, 5), 2, 128, False, BF, BF, "heads")
     g = rand(50, *q.shape, dt=BF), rand(51, *k.shape, dt=BF)

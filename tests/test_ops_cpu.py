@@ -115,6 +115,7 @@ def test_norm_backward_refuses():
     assert call(ws=0) == _lib.PARK_ERR_INVALID_ARG
     assert call(ws=FAKE + 8) == _lib.PARK_ERR_INVALID_ARG
     assert call(eps=0.0) == _lib.PARK_ERR_INVALID_ARG
+    assert call(eps=2.0 ** -81) == _lib.PARK_ERR_INVALID_ARG and norm(eps=2.0 ** -81) == _lib.PARK_ERR_INVALID_ARG
     assert call(heads=H + 1) == _lib.PARK_ERR_INVALID_ARG
 
 
