@@ -697,6 +697,15 @@ int launch_dense_dkv_reduce(const DenseArgs& a, int dtype, const DkvSplit& sp, i
     return PARK_OK;
 }
 
+// Parts are sized for the longest sequence that the bounds could hold, which the host does not know: a packed batch gets no
+// more of them than fit in 256 MB (its parts of one length are then longer).  Without packing 80 MB are never exceeded.
+static long long limit_chunk(long long chunk, long long steps, long long part_bytes) {
+    long long most = (256ll << 20) / (part_bytes > 0 ? part_bytes : 1);
+    if (most < 1) most = 1;
+    const long long least = (steps + most - 1) / most;
+    return chunk < least ? least : chunk;
+}
+
 // Few keys under many rows (text keys): the key tiles alone leave SMs idle, so the rows are split, about two CTAs for each
 // SM, at least 8 steps each.
 DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int n_seq, int D, int tile) {
@@ -711,6 +720,7 @@ DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int 
         const long long work = n_seq > 0 ? (steps + n_seq * G) * ((s.tiles + n_seq - 1) / n_seq) * Hk : steps * ctas;
         long long chunk = (work + waves * kDenseSMs - 1) / (waves * kDenseSMs);
         if (chunk < 8) chunk = 8;
+        chunk = limit_chunk(chunk, steps, 8ll * B * Hk * Nk * D);
         const long long n = (steps + chunk - 1) / chunk;  // (a sequence has at most all the steps)
         if (n > 1) {
             s.n = (int)n;
@@ -736,12 +746,13 @@ static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long 
     // keys would go from 38 to 43)
     if (chunk >= 32) chunk = (chunk + 1) / 2;
     if (chunk < least) chunk = least;
+    const size_t rows = (size_t)B * Hq * Nq;
+    chunk = limit_chunk(chunk, kt, 4ll * rows * (D + 1));
     const long long n = (kt + chunk - 1) / chunk;
     if (s->tiles * Hk * B * 2 <= kDenseSMs * wide && n > 1) {
         s->n = (int)n;
         s->chunk = (int)chunk;
     }
-    const size_t rows = (size_t)B * Hq * Nq;
     s->lse_off = s->n > 1 ? align_up((size_t)s->n * rows * D * 4, 256) : 0;
     s->bytes = s->n > 1 ? s->lse_off + align_up((size_t)s->n * rows * 4, 256) : 0;
 }

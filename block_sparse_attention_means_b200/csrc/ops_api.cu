@@ -94,6 +94,7 @@ int check_attn(const park_attn_shape* s, int Hq, int Hk) {
     if (s->n_seq > 0 && (s->B != 1 || !s->cu_q || !s->cu_k)) return PARK_ERR_INVALID_ARG;
     if (Hq > 65535 || s->B > 65535 || s->n_seq > (1 << 24)) return PARK_ERR_UNSUPPORTED;
     // rows of a key head's group, tiles and coordinates are int32
+    if (s->Nq >= kMaxRows || s->Nk >= kMaxRows) return PARK_ERR_UNSUPPORTED;  // (the products below stay in 64 bits)
     if (s->Nq * (Hq / Hk) >= kMaxRows - (1ll << 25) || s->Nk >= kMaxRows - (1ll << 25) ||
         (long long)s->B * Hq * (s->Nq / 8 + 1) >= kMaxRows || (long long)s->B * Hk * (s->Nk / 8 + 1) >= kMaxRows ||
         (long long)s->n_seq * Hq >= kMaxRows / 4)

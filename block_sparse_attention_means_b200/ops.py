@@ -29,11 +29,17 @@ _DT = {torch.bfloat16: _lib.PARK_BF16, torch.float32: _lib.PARK_F32}
 _status_words: dict[int, torch.Tensor] = {}
 
 
+def _device_index(device) -> int:
+    dev = torch.device("cuda" if device is None else device)  # (a number: that CUDA device)
+    if dev.type != "cuda":
+        raise ValueError(f"device {dev}: expected a CUDA device")
+    return torch.cuda.current_device() if dev.index is None else dev.index
+
+
 def status_word(device=None) -> torch.Tensor:
     """The device's default status word, int32 [1] (see include/park.h for the codes).
     Read it with ``.item()`` and clear it with ``.zero_()``."""
-    dev = torch.device("cuda" if device is None else device)
-    index = torch.cuda.current_device() if dev.index is None else dev.index
+    index = _device_index(device)
     if index not in _status_words:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the device has no status word yet: call status_word(device) before the capture, or "
@@ -41,7 +47,7 @@ def status_word(device=None) -> torch.Tensor:
         with torch.cuda.device(index):
             word = torch.zeros(1, dtype=torch.int32, device="cuda")
             torch.cuda.current_stream().synchronize()  # once: any stream may use it from here on
-        _status_words[index] = word
+        _status_words.setdefault(index, word)  # (another thread may have been first)
     return _status_words[index]
 
 
@@ -192,9 +198,7 @@ def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1
         raise ValueError("extent, pairs and scale have one entry for each of the three axes")
     if min(extent) < 1 or min(pairs) < 0 or sum(pairs) > D // 2:
         raise ValueError(f"extents {extent} must be positive and pairs {pairs} sum to at most D/2 = {D // 2}")
-    dev = torch.device("cuda" if device is None else device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch.device("cuda", _device_index(device))
     with _On(dev.index, stream) as st:
         r = Rope(extent, pairs, bool(half), torch.empty(0, dtype=torch.float32, device=dev))
         n = _lib.load().park_rope_table_floats(r.c())

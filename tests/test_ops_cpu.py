@@ -144,6 +144,9 @@ def attention(s=None, q=None, k=None, v=None, o=None, status=FAKE):
     (dict(s=shape(b=1, n_seq=2, cu_q=FAKE)), _lib.PARK_ERR_INVALID_ARG),
     (dict(s=shape(nk=1 << 31)), _lib.PARK_ERR_UNSUPPORTED),
     (dict(s=shape(nq=1 << 31)), _lib.PARK_ERR_UNSUPPORTED),
+    (dict(s=shape(nq=1 << 62), k=operand(0x100000, heads=1), v=operand(0x200000, heads=1)), _lib.PARK_ERR_UNSUPPORTED),
+    (dict(s=shape(b=4, nq=1 << 62)), _lib.PARK_ERR_UNSUPPORTED),
+    (dict(s=shape(b=4, nk=1 << 62)), _lib.PARK_ERR_UNSUPPORTED),
     (dict(k=operand(0x100000, heads=3), v=operand(0x200000, heads=3)), _lib.PARK_ERR_INVALID_ARG),
     (dict(v=operand(0x200000, heads=2)), _lib.PARK_ERR_INVALID_ARG),
     (dict(o=operand(0x300000, heads=2)), _lib.PARK_ERR_INVALID_ARG),
@@ -181,6 +184,31 @@ def test_attention_backward_refuses():
             assert call(bad=i, op=operand(0x900000, heads=2)) == _lib.PARK_ERR_INVALID_ARG
     for i in (5, 6, 7):
         assert call(bad=i, op=operand(0x900000, sh=D)) == _lib.PARK_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dt", [_lib.PARK_BF16, _lib.PARK_F32])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_attention_workspace_stays_small(dt, backward):
+    """Besides delta (4 bytes a row) the parts of a split take 256 MB and a little at most, whatever the sequences."""
+    lib, need = _lib.load(), ctypes.c_size_t(0)
+    for n_seq in (0, 1, 2, 31, 70, 500, 5000):
+        for nq in (1, 70, 2300, 9400, 32000, 200000):
+            for nk in (1, 70, 3000, 32000, 130000, 2000000):
+                for hq, hk in ((1, 1), (8, 1), (32, 1), (24, 8), (40, 40)):
+                    s = shape(b=1, d=128, dt=dt, nq=nq, nk=nk, n_seq=n_seq, cu_q=FAKE, cu_k=FAKE)
+                    assert lib.park_attention_workspace(s, hq, hk, backward, need) == _lib.PARK_OK
+                    parts = need.value - backward * 4 * hq * nq
+                    assert parts <= (256 << 20) + 4096, (n_seq, nq, nk, hq, hk, parts)
+                    if n_seq == 0:
+                        assert parts <= 80 << 20, (nq, nk, hq, hk, parts)
+
+
+@pytest.mark.parametrize("where", ["cpu", torch.device("cpu")])
+def test_host_devices_are_refused(where):
+    with pytest.raises(ValueError):
+        park.rope_table((2, 4, 5), 64, device=where)
+    with pytest.raises(ValueError):
+        park.status_word(where)
 
 
 def test_python_refuses_host_tensors():
