@@ -70,10 +70,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, limit_ns));
 }
-// Value of lane `src`'s pointer.
-__device__ __forceinline__ uint8_t* shfl_ptr(uint8_t* p, int src) {
-    return reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
-}
 // 2^x of a pair on the FMA pipe: x = n + r with n the nearest integer (from the low bits of x + 1.5 2^23)
 // and |r| <= 1/2, 2^r by its minimax polynomial of degree 4 in relative error (Remez exchange, 2^-18.5;
 // P is rounded to 2^-8 next), times 2^n.  x <= 128 here; below -127 the factor 2^n is 0.  NaN stays NaN.
