@@ -20,11 +20,10 @@
 namespace park {
 namespace {
 
-// Measured at 24 + 24 heads x 119,056 tokens and 40 + 40 x 75,600, D = 128, bf16.  Forward: 8 blocks of 4 warps 6.23 and
-// 6.21 TB/s (6 blocks 5.30 and 5.38, 12 with two rows in flight 5.97 and 6.04).  Backward: 4 blocks 5.92 and 6.22 TB/s (3
+// Measured at 24 + 24 heads x 119,056 tokens and 40 + 40 x 75,600, D = 128, bf16.  Forward: 8 blocks of 4 warps 6.30 and
+// 6.22 TB/s (6 blocks 5.30 and 5.38, 12 with two rows in flight 5.97 and 6.04).  Backward: 4 blocks 5.92 and 6.22 TB/s (3
 // blocks 5.31 and 5.68, 6 blocks 5.39 and 5.69: more warps at once write to more places at once).
 constexpr int kWarps = 4, kBlocks = 8;  // warps of a block, blocks of an SM
-constexpr int kUnroll = 4;              // head rows in flight for each lane group
 constexpr int kBwdWarps = 4, kBwdBlocks = 4, kBwdStages = 5;
 
 // The four pairs of a lane, as packed float32 pairs (one instruction for two elements): a[i] = the first
@@ -306,26 +305,30 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks)
     const int l = lane % LPR, grp = lane / LPR;
     const bool active = 8 * l < D;
     constexpr int RPW = 32 / LPR;  // rows of a warp step
+    constexpr int kUnroll = 64 / sizeof(Raw<T>);  // rows in flight for each lane group: 64 bytes a lane fit the registers
+    Raw<T> raw[kUnroll];
+    auto load = [&](int u, int hh) {
+        if (hh < h1 && active) {
+            load_raw<HALF>(raw[u], x + hh * xh, l, D);
+        } else {
+#pragma unroll
+            for (uint32_t& v : raw[u].v) v = 0u;
+        }
+    };
+    // The first rows travel while the angles are looked up, the next ones while these are worked on (12 + 12 heads x 37,800
+    // tokens, D = 128: the rotation of bf16 heads 5.0 -> 5.4 TB/s, norm and rotation in float32 5.6 -> 6.1, in bf16 4.8 -> 4.9).
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) load(u, h0 + grp + u * RPW);
     const Turn turn = token_angles(rp, b, n, l, active, sign, status);
     Quad w;
     if (NORM) w = load_weights<HALF>(isk ? k.w : q.w, wdtype, l, D, active);
     const float inv_d = 1.f / (float)D;
     for (int h = h0 + grp; h - grp < h1; h += RPW * kUnroll) {
-        Raw<T> raw[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int hh = h + u * RPW;
-            if (hh < h1 && active) {
-                load_raw<HALF>(raw[u], x + hh * xh, l, D);
-            } else {
-#pragma unroll
-                for (uint32_t& v : raw[u].v) v = 0u;
-            }
-        }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int hh = h + u * RPW;
             Quad v = unpack<HALF>(raw[u]);
+            load(u, hh + RPW * kUnroll);
             if (NORM) {
                 const float r = rsqrtf(row_sum<LPR>(dot(v, v)) * inv_d + eps);
                 v = mul(v, mul(w, r));
