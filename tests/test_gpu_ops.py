@@ -523,6 +523,52 @@ def test_hidden_keys_and_values_do_not_reach_a_row(dt, bad):
     assert torch.equal(grads[2][:, :, hidden], ggrads[2][:, :, hidden])
 
 
+def test_gradient_of_a_dominant_key():
+    """Every row gives one key a p halfway between two bf16 numbers: rounded to bf16 it would be 2^-8 off in every term of
+    dv, in the same direction.  A key like that gets 16 bits from its third step of 128 rows on, so the sum over 4,096 rows is
+    off by 256 / 4096 of 2^-8, 2^-16 for the second rounding, p's own error and the sum's: the result is the rounding of
+    a number within that of the value."""
+    n, D, at = 4096, 128, 77
+    scale = float(np.float32(math.log(0.501953125 / 0.498046875 * (n - 1)) / 8))
+    q, k, v = torch.zeros(1, 1, n, D), torch.zeros(1, 1, n, D), rand(330, 1, 1, n, D, dt=BF)
+    q[..., 0], k[0, 0, at, 0] = 1, 8
+    q, k = q.to(BF).cuda(), k.to(BF).cuda()
+    do = rand(331, 1, 1, 1, D, dt=BF).expand(1, 1, n, D).contiguous()
+    o, lse = park.attention(q, k, v, scale=scale, return_lse=True)
+    dv = park.attention_bwd(do, q, k, v, o, lse, scale=scale)[2][0, 0, at].double()
+    t = 8 * scale
+    p = 1 / (1 + (n - 1) * math.exp(-t))
+    want = n * p * do[0, 0, 0].double()
+    es = (D + 4) * E * t
+    rp = es + 2 * es + (96 + math.log2(n)) * E + n * E + 4 * E * (1 + t) + 96 * E
+    e = (256 / n * U[BF] + 2 ** -16 + rp + (n + 4) * E) * want.abs()
+    low, high = (want - e).to(BF).double(), (want + e).to(BF).double()
+    assert ((dv >= low) & (dv <= high)).all()
+    # the bound tells the difference: most columns would be outside with p rounded once
+    once = (want * (0.5 / p)).to(BF).double()
+    assert ((once < low) | (once > high)).float().mean() > 0.5
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_dominant_keys_in_every_place(causal, D):
+    """Keys that draw most of the attention in whole and in cut tiles, for heads that share them, packed."""
+    lens = [2300, 40, 1000]
+    N = sum(lens)
+    q, k, v, do = (rand(340 + i, 1, h, N, D, dt=BF) for i, h in enumerate((4, 2, 2, 4)))
+    u = rand(345, D)
+    q = (q + 0.7 * u).to(BF)
+    for key in (0, 130, 2299, 2320, 2340, 2700):
+        k[0, :, key] = (u * (5 + key % 3)).to(BF)
+    cu = cu_of(lens)
+    o, lse = park.attention(q, k, v, causal=causal, cu_q=cu, cu_k=cu, return_lse=True)
+    grads = park.attention_bwd(do, q, k, v, o, lse, causal=causal, cu_q=cu, cu_k=cu)
+    bounds = cu.tolist()
+    attn_check(q, k, v, o, lse, causal, 1 / math.sqrt(D), BF, do, grads, (bounds, bounds))
+    again = park.attention_bwd(do, q, k, v, o, lse, causal=causal, cu_q=cu, cu_k=cu)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
 def test_attention_scores_of_large_range():
     """Scores over hundreds of log2 units: the running maximum moves by far more than a tile's spread."""
     n, D = 600, 128
