@@ -24,8 +24,8 @@
 // the errors of dq and dk were 7.5e-3 and 6e-3 of their norms without this.
 //
 // In both, 256 threads work on a 128 x 128 tile, two on a row with 64 columns each; the
-// half h of a bf16 operand lies on the first 32 of its own 64 columns, so a thread only
-// overwrites what it has read itself.  p and ds are rounded to bf16 as operands.
+// half h of a bf16 operand lies on the first 32 of its own 64 columns (a second part on the
+// others), so a thread only overwrites what it has read itself.  p and ds are rounded to bf16 as operands.
 //
 // Tiles that a mask cuts are cleaned by the same threads before the product that sums
 // over the hidden rows: infinities and NaN become 0 (0 x NaN is NaN); what visible rows
@@ -88,10 +88,10 @@ __device__ __forceinline__ void hide(uint32_t (&pk)[N], int c0, int lo, int hi) 
 
 // A key that draws kDominant times its share of the rows' attention gives a row of dv (and of dk) so much larger than the others
 // that the roundings of p and ds to bf16 in it stand out in the tensor as a whole.  Two steps after one is seen, its
-// tile's p and ds get a second bf16 part and a second product.  75,600 rows whose scores reach +-30, where single keys hold
-// half of dv's norm: dv and dk were 2.3e-3 and 2.5e-3 of their norms off, now 1.7e-3, which is the rounding of the result.
+// tile's p and ds get a second bf16 part and a second product.  75,600 rows of which many attend to the same few
+// keys, one of them with half of dv's norm: dv and dk were 2.3e-3 and 2.5e-3 of their norms off, now 1.7e-3, which is the rounding of the result.
 // Where no key is dominant, the looking costs the dk/dv kernel 1.5 % (D = 128: 3.07 -> 3.12 ms at 32,768 x 4 heads) to 6 %
-// (D = 64: 338 -> 358 us at 8,192 causal, 16/4 heads); looking at every step, 3 to 8 %.
+// (D = 64: 338 -> 358 us at 8,192 causal, 16/4 heads).
 constexpr float kDominant = 64.f;
 constexpr int kSample = 8;  // steps of which one is looked at
 
