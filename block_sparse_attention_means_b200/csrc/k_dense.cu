@@ -781,7 +781,10 @@ DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, i
     else
         s.rows = mean < 32 || dense_tiles(rows, n_seq, 16) * kt * Hk * B <= 2 * kDenseSMs ? 16 : 64;
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + TB - 1) / TB + n_seq, n_seq, D, 4, 2, 1);
+    // Parts of one key tile only while those fill no more than the SMs (captured: 256 x 2,048 keys, one head, D = 64, 14 us and
+    // 19 with two; 1 x 500 x 8 heads, D = 128, 11 and 18; but 300 x 1,000 x 2 heads 33 and 28, 512^2 x 8, D = 64, 34 and 28)
+    const long long keys = (Nk + TB - 1) / TB + n_seq;
+    split_keys(&s, B, Hq, Hk, Nq, keys, n_seq, D, 4, 2, s.tiles * Hk * B * keys > kDenseSMs ? 2 : 1);
     return s;
 }
 
