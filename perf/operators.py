@@ -65,7 +65,7 @@ def listed():
         # a training step of the Wan-shaped layer's norms: outputs and all gradients
         _norm_case("norm_rope_wan_train_bf16", H=40, Hk=40, T=21, Hg=45, W=80, train=True),
         # odd sizes in float32: batch, grouped heads, a head width that fills no power of two
-        _norm_case("norm_rope_odd_train_f32", dtype="f32", B=3, H=10, Hk=5, T=7, Hg=19, W=23, text=14, D=96, train=True),
+        _norm_case("norm_rope_odd_train_f32", dtype="f32", B=3, H=10, Hk=5, T=7, Hg=19, W=23, text=13, D=96, train=True),
         # the smallest attention call: the tiny layer
         _attn_case("attn_tiny_f32", dtype="f32", H=1, Hk=1, D=64, lq="256", lk="256", packed=False),
         # one new row for each of four clips that are at different points: every key is read for one query
