@@ -289,14 +289,13 @@ __global__ void __launch_bounds__(256)
     float M = -INFINITY;
     for (int s = lane; s < n_split; s += 32) M = fmaxf(M, part_lse[s * rows_all + id]);
     M = warp_max(M);
-    const bool none = M == -INFINITY;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
 #pragma unroll 4
     for (int s = w0; s < n_split; s += W) {
         const float ls = part_lse[s * rows_all + id];
         if (ls == -INFINITY) continue;  // (its part of o may not be written)
-        const float w = exp2f(ls - M);
+        const float w = exp2f(ls - M);  // (NaN where the row's scores are: M, which leaves NaN out, may be -inf then)
         sum += w;
         if (4 * lane < a.D) {
             const float4 o = *reinterpret_cast<const float4*>(part_o + (s * rows_all + id) * a.D + 4 * lane);
@@ -317,6 +316,7 @@ __global__ void __launch_bounds__(256)
             sum += sh_sum[i];
         }
     }
+    const bool none = M == -INFINITY && sum == 0.f;  // no visible key
     const float inv = none ? 0.f : 1.f / sum;
     if (4 * lane < a.D)
         store4<T>(row_ptr<T>(a.o, b, head, t.q0 + tok), lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));

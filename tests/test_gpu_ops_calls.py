@@ -1,0 +1,28 @@
+"""Calls of the operators and of layer(pre=...) beyond the plain one: rows of NaN where the keys are split, conditions
+that reach the result's status, objects made on one stream and used on another."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_means_b200 as park
+from block_sparse_attention_means_b200 import _lib
+from test_gpu_ops import BF, F32, angles, attn_inputs, clean_status, grid_positions, pair_mass, plain_rotate, rand, within  # noqa: F401
+from test_gpu_ops import E, U
+
+pytestmark = pytest.mark.gpu
+
+
+# 3 to 4 parts (joined by one warp a row) and more than 4 (by eight); 300 x 300 x 30 is not split
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("H,nq,nk", [(1, 2, 1000), (1, 2, 6000), (30, 300, 300)])
+def test_a_query_row_of_nan(dt, H, nq, nk):
+    """Its o and lse are NaN however the keys are split; the other rows keep their bits."""
+    q, k, v, _ = attn_inputs(1, H, H, nq, nk, 64, dt, "heads")
+    good, glse = park.attention(q, k, v, return_lse=True)
+    q[0, 0, 1] = float("nan")
+    o, lse = park.attention(q, k, v, return_lse=True)
+    assert o[0, 0, 1].isnan().all() and lse[0, 0, 1].isnan()
+    keep = torch.ones(1, H, nq, dtype=torch.bool, device="cuda")
+    keep[0, 0, 1] = False
+    assert torch.equal(o[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
