@@ -177,10 +177,15 @@ def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torc
           out: Retrieval | None = None, ws: torch.Tensor | None = None, stream=None, pre=None):
     """Retrieval + block-sparse attention; returns (O, Retrieval).  pre (an ops.NormRope):
     Q and K are the raw projections, in any layout that the operators take, and are
-    normed and rotated first; conditions that pre meets go to the result's status word
-    of ops.status_word(device)."""
+    normed and rotated first; a condition that pre meets (a position out of range leaves
+    its token unrotated) is in the result's status like the layer's own, which come first."""
+    met = None
     if pre is not None:
-        Q, K = pre(Q, K, stream=stream)
+        if not Q.is_cuda:
+            raise ValueError(f"Q: expected a CUDA tensor, got one on {Q.device}")
+        with torch.cuda.stream(stream):
+            met = torch.zeros(1, dtype=torch.int32, device=Q.device)
+        Q, K = pre(Q, K, status=met, stream=stream)
     _check_inputs(shape, Q, K, V)
     O = O if O is not None else torch.empty_like(Q)
     out = out or alloc_retrieval(shape, NQ, NK, Q.device)
@@ -191,6 +196,9 @@ def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torc
                                 ctypes.c_void_p(O.data_ptr()), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
                                 ws.numel(), _stream(stream))
     _lib.check(rc, "park_layer")
+    if met is not None:  # (retrieval clears the status word first, so what pre met is added last)
+        with torch.cuda.stream(stream):
+            torch.where(out.status == 0, met, out.status, out=out.status)
     return O, out
 
 

@@ -26,3 +26,25 @@ def test_a_query_row_of_nan(dt, H, nq, nk):
     keep = torch.ones(1, H, nq, dtype=torch.bool, device="cuda")
     keep[0, 0, 1] = False
     assert torch.equal(o[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_layer_reports_what_pre_meets(norm):
+    """A position out of range leaves its token unrotated: the layer's own result says so, the next one is good again."""
+    B, H, T, Hg, W, text, D = 1, 2, 4, 8, 8, 16, 128
+    shape = park.Shape(B, H, T, Hg, W, text, D)
+    q, k, v = (rand(700 + i, B, H, shape.N, D, dt=BF) for i in range(3))
+    pos = grid_positions((T, Hg, W), shape.N).to(torch.int32).contiguous()
+    bad = pos.clone()
+    bad[9] = torch.tensor([0, Hg, 0])
+    r = park.rope_table((T, Hg, W), D)
+    args = (q, k, v, shape, 8, 8, 0.9, 3)
+    out = None
+    for p, code in ((bad, _lib.PARK_ERR_INDEX), (pos, _lib.PARK_OK), (bad, _lib.PARK_ERR_INDEX)):
+        pre = park.NormRope(rope=r, positions=p.cuda(), norm=norm)
+        _, out = park.layer(*args, out=out, pre=pre)
+        assert out.status_code() == code
+    # what the layer itself meets comes first
+    v[0, 0, 3, 3] = float("nan")
+    _, out = park.layer(*args, out=out, pre=pre)
+    assert out.status_code() == _lib.PARK_ERR_RANGE
