@@ -189,7 +189,8 @@ def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1
     and kept.  extent = (frames, rows, columns); pairs defaults to the split of D/2
     that the synthetic layers use: a third each for rows and columns, the rest for
     time (22/21/21 at D = 128).  For plain 1-D positions pass extent (n, 1, 1) and
-    pairs (D/2, 0, 0)."""
+    pairs (D/2, 0, 0).  The call returns when the table is filled, so that any stream may
+    use it at once; inside a capture it does not wait, and the graph fills the table."""
     if pairs is None:
         third = D // 2 // 3
         pairs = (D // 2 - 2 * third, third, third)
@@ -205,7 +206,9 @@ def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1
         r.table = torch.empty(max(2, n), dtype=torch.float32, device=dev)
         rc = _lib.load().park_rope_table(r.c(), float(theta),
                                          (ctypes.c_double * 3)(*[float(x) for x in scale]), st)
-    _lib.check(rc, "park_rope_table")
+        _lib.check(rc, "park_rope_table")
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()  # once: any stream may use it from here on
     return r
 
 

@@ -48,3 +48,32 @@ def test_layer_reports_what_pre_meets(norm):
     v[0, 0, 3, 3] = float("nan")
     _, out = park.layer(*args, out=out, pre=pre)
     assert out.status_code() == _lib.PARK_ERR_RANGE
+
+
+def test_rope_table_used_at_once_on_another_stream():
+    """A table made on a stream that is still busy is whole when the call that made it returns."""
+    D, extent = 64, (40, 30, 20)
+    x = rand(710, 1, 2, math.prod(extent), D)
+    c, s = angles(extent, (12, 10, 10), 10000.0, (1, 1, 1), grid_positions(extent, x.shape[2]))
+    want = plain_rotate(x.double(), c, s, False)
+    park.rope(x, park.rope_table(extent, D))    # (the kernels are loaded: loading one may wait for the device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.full((2 * (40 * 12 + 30 * 10 + 20 * 10),), 3.0, device="cuda")  # what the table's memory holds before
+        torch.cuda._sleep(400_000_000)                                       # about 0.2 s
+    r = park.rope_table(extent, D, stream=side)
+    y = park.rope(x, r)
+    within(y, want, U[F32] * want.abs() + 4 * E * pair_mass(x.double(), False))
+
+
+def test_rope_table_in_a_capture():
+    """Inside a capture nothing waits: the graph fills the table."""
+    x = rand(711, 1, 2, 24, 64)
+    want = park.rope(x, park.rope_table((2, 3, 4), 64))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = park.rope(x, park.rope_table((2, 3, 4), 64))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
