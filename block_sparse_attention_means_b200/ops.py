@@ -175,12 +175,24 @@ class Rope:
     table: torch.Tensor      # float32, (cos, sin) of every position of every axis
 
     def c(self) -> _lib.ParkRopeAxes:
-        key = (self.extent, self.pairs, self.half, self.table.data_ptr())
+        t = self.table
+        key = (self.extent, self.pairs, self.half, t.data_ptr(), t.numel(), t.dtype)
         made = self.__dict__.get("_c")
         if made is None or made[0] != key:
-            i3 = ctypes.c_int * 3
-            made = self.__dict__["_c"] = (key, _lib.ParkRopeAxes(i3(*self.extent), i3(*self.pairs), self.half, key[3]))
+            axes = _axes(self.extent, self.pairs, self.half, key[3])
+            need = _lib.load().park_rope_table_floats(axes)
+            if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < need:
+                raise ValueError(f"rope table: expected {need} contiguous float32 values for extents {self.extent} and "
+                                 f"pairs {self.pairs}, got {t.numel()} of {t.dtype}")
+            made = self.__dict__["_c"] = (key, axes)
         return made[1]
+
+
+def _axes(extent, pairs, half, table) -> _lib.ParkRopeAxes:
+    if len(extent) != 3 or len(pairs) != 3:
+        raise ValueError("extent and pairs have one entry for each of the three axes")
+    i3 = ctypes.c_int * 3
+    return _lib.ParkRopeAxes(i3(*extent), i3(*pairs), bool(half), table)
 
 
 def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1.0, 1.0), half: bool = False,
@@ -201,9 +213,8 @@ def rope_table(extent, D: int, pairs=None, theta: float = 10000.0, scale=(1.0, 1
         raise ValueError(f"extents {extent} must be positive and pairs {pairs} sum to at most D/2 = {D // 2}")
     dev = torch.device("cuda", _device_index(device))
     with _On(dev.index, stream) as st:
-        r = Rope(extent, pairs, bool(half), torch.empty(0, dtype=torch.float32, device=dev))
-        n = _lib.load().park_rope_table_floats(r.c())
-        r.table = torch.empty(max(2, n), dtype=torch.float32, device=dev)
+        n = _lib.load().park_rope_table_floats(_axes(extent, pairs, half, None))
+        r = Rope(extent, pairs, bool(half), torch.empty(max(2, n), dtype=torch.float32, device=dev))
         rc = _lib.load().park_rope_table(r.c(), float(theta),
                                          (ctypes.c_double * 3)(*[float(x) for x in scale]), st)
         _lib.check(rc, "park_rope_table")

@@ -222,3 +222,30 @@ def test_python_refuses_host_tensors():
         park.attention(x, x, x)
     with pytest.raises(ValueError):
         park.attention_bwd(x, x, x, x, x, x)
+
+
+@pytest.mark.parametrize("table", [
+    torch.zeros(127), torch.zeros(0), torch.zeros(128, dtype=torch.float64), torch.zeros(256)[::2],
+])
+def test_a_rope_whose_table_does_not_fit_its_axes_is_refused(table):
+    """The kernels index the table by the axes: 4 positions of 16 pairs are 128 values."""
+    with pytest.raises(ValueError):
+        park.Rope((4, 1, 1), (16, 0, 0), False, table).c()
+    good = park.Rope((4, 1, 1), (16, 0, 0), False, torch.zeros(128))
+    assert good.c() is good.c()
+    good.extent = (5, 1, 1)
+    with pytest.raises(ValueError):
+        good.c()
+    good.extent, good.table = (4, 1, 1), table
+    with pytest.raises(ValueError):
+        good.c()
+    with pytest.raises(ValueError):
+        park.Rope((4, 1), (16, 0), False, torch.zeros(128)).c()
+
+
+def test_a_narrower_view_of_the_table_is_refused():
+    r = park.Rope((4, 1, 1), (16, 0, 0), False, torch.zeros(128))
+    r.c()
+    r.table = r.table[:64]
+    with pytest.raises(ValueError):
+        r.c()
