@@ -187,6 +187,9 @@ class Rope:
             made = self.__dict__["_c"] = (key, axes)
         return made[1]
 
+    def __getstate__(self):  # copies and pickles make their own C struct
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+
 
 def _axes(extent, pairs, half, table) -> _lib.ParkRopeAxes:
     if len(extent) != 3 or len(pairs) != 3:

@@ -1,6 +1,8 @@
 """Refusals of the operators before and beside the layer, without a GPU: every bad
 argument is answered on the host, before anything is enqueued."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -249,3 +251,14 @@ def test_a_narrower_view_of_the_table_is_refused():
     r.table = r.table[:64]
     with pytest.raises(ValueError):
         r.c()
+
+
+@pytest.mark.parametrize("again", [copy.copy, copy.deepcopy, lambda r: pickle.loads(pickle.dumps(r))])
+def test_a_rope_in_use_can_be_copied(again):
+    r = park.Rope((4, 1, 1), (16, 0, 0), True, torch.arange(128.0))
+    r.c()
+    s = again(r)
+    assert (s.extent, s.pairs, s.half) == (r.extent, r.pairs, r.half) and torch.equal(s.table, r.table)
+    assert s.c().table == s.table.data_ptr() and r.c().table == r.table.data_ptr()
+    n = again(park.NormRope(torch.ones(64), None, rope=r, eps=1e-5))
+    assert n.eps == 1e-5 and torch.equal(n.q_weight, torch.ones(64)) and torch.equal(n.rope.table, r.table)
