@@ -4,7 +4,8 @@ every step of the computation runs in the library's CUDA kernels.
 The names follow the C ABI: ``workspace_size``, ``retrieve``, ``sparse_attn``,
 ``layer``.  Tensors are [B, H, N, D], contiguous, on one CUDA device, in
 torch.bfloat16 or torch.float32 with D a multiple of 32 up to 128 (bf16 with
-D = 128 runs the tensor-core kernels).
+D = 128 runs the tensor-core kernels).  Temporary memory and outputs that the
+caller does not pass come from the stream that the call runs on.
 """
 from __future__ import annotations
 
@@ -145,11 +146,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocating_on(stream):
+    """What a call allocates (workspace, outputs and their zeros) belongs to the stream that it
+    runs on: the memory of a workspace that is dropped on return is then not handed out while
+    the call's kernels still use it.  None: the current stream."""
+    return torch.cuda.stream(stream)
+
+
 def retrieve(Q, K, shape: Shape, NQ: int, NK: int, p: float, iters: int, out: Retrieval | None = None,
              ws: torch.Tensor | None = None, stream=None) -> Retrieval:
     _check_inputs(shape, Q, K)
-    out = out or alloc_retrieval(shape, NQ, NK, Q.device)
-    ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
+    with _allocating_on(stream):
+        out = out or alloc_retrieval(shape, NQ, NK, Q.device)
+        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
     s, r = shape.c(), out.c()
     rc = _lib.load().park_retrieve(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()), ctypes.byref(s),
                                    NQ, NK, float(p), int(iters), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
@@ -161,9 +170,10 @@ def retrieve(Q, K, shape: Shape, NQ: int, NK: int, p: float, iters: int, out: Re
 def sparse_attn(Q, K, V, shape: Shape, NQ: int, NK: int, r: Retrieval, O: torch.Tensor | None = None,
                 ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _check_inputs(shape, Q, K, V)
-    O = O if O is not None else torch.empty_like(Q)
+    with _allocating_on(stream):
+        O = O if O is not None else torch.empty_like(Q)
+        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
     _check_inputs(shape, O)
-    ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
     s, rc_ = shape.c(), r.c()
     rc = _lib.load().park_sparse_attn(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
                                       ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, ctypes.byref(rc_),
@@ -183,13 +193,14 @@ def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torc
     if pre is not None:
         if not Q.is_cuda:
             raise ValueError(f"Q: expected a CUDA tensor, got one on {Q.device}")
-        with torch.cuda.stream(stream):
+        with _allocating_on(stream):
             met = torch.zeros(1, dtype=torch.int32, device=Q.device)
         Q, K = pre(Q, K, status=met, stream=stream)
     _check_inputs(shape, Q, K, V)
-    O = O if O is not None else torch.empty_like(Q)
-    out = out or alloc_retrieval(shape, NQ, NK, Q.device)
-    ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
+    with _allocating_on(stream):
+        O = O if O is not None else torch.empty_like(Q)
+        out = out or alloc_retrieval(shape, NQ, NK, Q.device)
+        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
     s, r = shape.c(), out.c()
     rc = _lib.load().park_layer(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
                                 ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, float(p), int(iters),
@@ -197,7 +208,7 @@ def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torc
                                 ws.numel(), _stream(stream))
     _lib.check(rc, "park_layer")
     if met is not None:  # (retrieval clears the status word first, so what pre met is added last)
-        with torch.cuda.stream(stream):
+        with _allocating_on(stream):
             torch.where(out.status == 0, met, out.status, out=out.status)
     return O, out
 

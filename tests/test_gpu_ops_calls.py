@@ -77,3 +77,31 @@ def test_rope_table_in_a_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_the_layer_on_a_busy_stream():
+    """What the call allocates and drops (workspace, normed queries and keys) is not handed out to others before it has
+    run: the current stream allocates and fills as much while the call waits behind other work."""
+    B, H, T, Hg, W, text, D = 1, 2, 4, 8, 8, 16, 128
+    shape = park.Shape(B, H, T, Hg, W, text, D)
+    q, k, v = (rand(720 + i, B, H, shape.N, D, dt=BF) for i in range(3))
+    pre = park.NormRope(rope=park.rope_table((T, Hg, W), D))
+    a, b = pre(q, k)
+    want, r = park.layer(a, b, v, shape, 8, 8, 0.9, 3)
+    size = park.workspace_size(shape, 8, 8)
+    side = torch.cuda.Stream()
+    calls = (lambda: park.layer(q, k, v, shape, 8, 8, 0.9, 3, stream=side, pre=pre)[0],
+             lambda: park.layer(a, b, v, shape, 8, 8, 0.9, 3, stream=side)[0],
+             lambda: park.sparse_attn(a, b, v, shape, 8, 8, r, stream=side),
+             lambda: park.retrieve(a, b, shape, 8, 8, 0.9, 3, stream=side).mask)
+    for call, res in zip(calls, (want, want, want, r.mask)):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)               # about 0.1 s
+        got = call()
+        over = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        over += [torch.full_like(t, 7.0) for t in (q, k, q, k)]
+        assert not side.query()
+        torch.cuda.synchronize()
+        assert torch.equal(got, res)
