@@ -621,7 +621,7 @@ int fwd_simt_r(const DenseArgs& a, const DenseSplit& sp, float* part_o, float* p
     ::park::prof_begin(st);
     k_dense_fwd_simt<D, R><<<dim3((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n), 256, sm, st>>>(
         a, dense_order(a, sp.tiles, a.B * a.Hk, 8 * a.Nk * D, 1), sp.n, sp.chunk, part_o, part_lse);
-    PARK_TRY_LAUNCH("k_dense_fwd_simt", st);
+    PARK_TRY_LAUNCH(R == 8 ? "k_dense_fwd_simt, 128 rows" : R == 4 ? "k_dense_fwd_simt, 64 rows" : "k_dense_fwd_simt, 16 rows", st);
     return PARK_OK;
 }
 

@@ -487,7 +487,7 @@ int fwd_tc(const DenseArgs& a, const CUtensorMap& mK, const CUtensorMap& mV, con
     const dim3 grid((unsigned)(sp.tiles * a.B * a.Hk), 1, sp.n);
     ::park::prof_begin(st);
     k_dense_fwd_tc<NP, NS><<<grid, C::threads, C::smem, st>>>(mK, mV, a, order, sp.n, sp.chunk, part_o, part_lse, wait_limit_ns());
-    PARK_TRY_LAUNCH("k_dense_fwd_tc", st);
+    PARK_TRY_LAUNCH(NS == 2 ? "k_dense_fwd_tc, 256 rows" : "k_dense_fwd_tc, 128 rows", st);
     return PARK_OK;
 }
 
