@@ -734,17 +734,12 @@ DkvSplit dense_split_dkv(int B, int Hq, int Hk, long long Nq, long long Nk, int 
 }
 
 // Splits the keys when the row tiles alone leave SMs idle: parts of equal length whatever the sequence (a packed batch
-// holds at most kt key tiles in all, a batch entry has as many), about `waves` CTAs for each SM, at least `least` key
-// tiles each; done when the row tiles are at most `wide` CTAs for two SMs.
-static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long long kt, int n_seq, int D, int waves, int wide,
+// holds at most kt key tiles in all, a batch entry has as many), of `chunk` key tiles, at least `least`; done when the row
+// tiles are at most `wide` CTAs for two SMs.
+static void split_keys(DenseSplit* s, int B, int Hq, int Hk, long long Nq, long long kt, int D, long long chunk, int wide,
                        int least) {
     s->n = 1;
     s->chunk = 0;
-    const long long work = n_seq > 0 ? kt * Hk : kt * Hk * B * s->tiles;
-    long long chunk = (work + (long long)waves * kDenseSMs - 1) / ((long long)waves * kDenseSMs);
-    // long parts in twice as many CTAs (four sequences of 3,601 to 119,056 keys, 24/8 heads: 187 -> 174 us; 8 heads x 30,000
-    // keys would go from 38 to 43)
-    if (chunk >= 32) chunk = (chunk + 1) / 2;
     if (chunk < least) chunk = least;
     const size_t rows = (size_t)B * Hq * Nq;
     chunk = limit_chunk(chunk, kt, 4ll * rows * (D + 1));
@@ -765,7 +760,19 @@ DenseSplit dense_split_tc(int B, int Hq, int Hk, long long Nq, long long Nk, int
     const long long rows = Nq * (Hq / Hk);
     s.rows = dense_tiles(rows, n_seq, 256) * Hk * B * 2 <= kDenseSMs ? 128 : 256;
     s.tiles = dense_tiles(rows, n_seq, s.rows);
-    split_keys(&s, B, Hq, Hk, Nq, (Nk + 127) / 128 + n_seq, n_seq, D, 2, 1, 3);
+    // As many parts as run at once, two CTAs an SM: a few more start last and run alone.  In a packed batch (of single rows, one
+    // row tile each) every sequence may have a part that is not full, so kt / chunk + n_seq parts fit, and not less than half as
+    // many full ones.  24/8 heads, one row each, D = 128 and 64, captured, against parts that only come near that number: 119,056 +
+    // 75,600 + 40,001 + 3,601 keys 178 and 143 us against 205 and 162, 119,056 + 40,001 129 and 94 against 135 and 102, 8 x 16,000
+    // 115 and 90 against 125 and 94, 200,000 148 and 102 both, 4 x 60,000 176 and 131 against 176 and 125.  Parts of half the
+    // length: 195 and 154, 141 and 109, 150 and 121, 156 and 111, 190 and 141.  8 heads x 1,100 rows x 20,000 keys 115 and 102
+    // against 119 and 102, 300 x 119,056 199 and 178 against 193 and 174; 4 heads x 2,000 x 75,600 342 and 309 against 356 and
+    // 317 (half the length 328 and 291).
+    const long long kt = (Nk + 127) / 128 + n_seq, per = n_seq > 0 ? Hk : Hk * B * s.tiles;
+    const long long fit = 2 * kDenseSMs / (per > 0 ? per : 1);  // (no rows: no tiles)
+    long long parts = n_seq > 0 && fit - n_seq < fit / 2 ? fit / 2 : fit - n_seq;
+    if (parts < 1) parts = 1;
+    split_keys(&s, B, Hq, Hk, Nq, kt, D, (kt + parts - 1) / parts, 1, 3);
     return s;
 }
 
@@ -784,7 +791,11 @@ DenseSplit dense_split_simt(int B, int Hq, int Hk, long long Nq, long long Nk, i
     // Parts of one key tile only while those fill no more than the SMs (captured: 256 x 2,048 keys, one head, D = 64, 14 us and
     // 19 with two; 1 x 500 x 8 heads, D = 128, 11 and 18; but 300 x 1,000 x 2 heads 33 and 28, 512^2 x 8, D = 64, 34 and 28)
     const long long keys = (Nk + TB - 1) / TB + n_seq;
-    split_keys(&s, B, Hq, Hk, Nq, keys, n_seq, D, 4, 2, s.tiles * Hk * B * keys > kDenseSMs ? 2 : 1);
+    // About four blocks an SM (parts that fit as above: 8 heads, one row each, D = 128: 8 x 16,000 keys 666 us against 604, 4 x
+    // 30,000 584 and 565, 100,000 481 and 479)
+    const long long work = n_seq > 0 ? keys * Hk : keys * Hk * B * s.tiles;
+    split_keys(&s, B, Hq, Hk, Nq, keys, D, (work + 4 * kDenseSMs - 1) / (4 * kDenseSMs), 2,
+               s.tiles * Hk * B * keys > kDenseSMs ? 2 : 1);
     return s;
 }
 

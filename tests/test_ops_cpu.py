@@ -262,3 +262,18 @@ def test_a_rope_in_use_can_be_copied(again):
     assert s.c().table == s.table.data_ptr() and r.c().table == r.table.data_ptr()
     n = again(park.NormRope(torch.ones(64), None, rope=r, eps=1e-5))
     assert n.eps == 1e-5 and torch.equal(n.q_weight, torch.ones(64)) and torch.equal(n.rope.table, r.table)
+
+
+@pytest.mark.parametrize("dt, waves", [(_lib.PARK_BF16, 2), (_lib.PARK_F32, 4)])
+@pytest.mark.parametrize("hq, hk", [(24, 8), (8, 8), (5, 5)])
+@pytest.mark.parametrize("nk", [20000, 60000, 100000, 200000, 400000, 1000000])
+def test_single_rows_split_their_keys_into_whole_waves(dt, waves, hq, hk, nk):
+    """One row over many keys: about `waves` blocks for each SM at every length (bf16: no more, they run at once), read off
+    the parts' workspace."""
+    lib, need, d = _lib.load(), ctypes.c_size_t(0), 128
+    s = shape(b=1, d=d, dt=dt, nq=1, nk=nk)
+    assert lib.park_attention_workspace(s, hq, hk, 0, need) == _lib.PARK_OK
+    parts = need.value // (hq * (d + 1) * 4)
+    tile = 128 if dt == _lib.PARK_BF16 else 64
+    least = min(waves * 148, (nk + tile - 1) // tile * hk / 4)   # (parts of a few tiles at least)
+    assert least / 1.5 - hk <= parts * hk <= waves * 148 + (hk if dt == _lib.PARK_F32 else 0)
