@@ -90,7 +90,9 @@ __device__ __forceinline__ void hide(uint32_t (&pk)[N], int c0, int lo, int hi) 
 // that the roundings of p and ds to bf16 in it stand out in the tensor as a whole.  Two steps after one is seen, its
 // tile's p and ds get a second bf16 part and a second product.  75,600 rows of which many attend to the same few
 // keys, one of them with half of dv's norm: dv and dk were 2.3e-3 and 2.5e-3 of their norms off, now 1.7e-3, which is the rounding of the result.
-// Where no key is dominant, the looking costs the dk/dv kernel 1.5 % (D = 128: 3.07 -> 3.12 ms at 32,768 x 4 heads) to 6 %
+// Steps that a mask cuts are not looked at, and nothing changes before the third step: in sequences of a few tiles a row of
+// dv cannot outweigh the others by so much.  dq needs nothing like it, its rows are averages.
+// Where no key is dominant, the looking costs the dk/dv kernel alone 1.5 % (D = 128: 3.07 -> 3.12 ms at 32,768 x 4 heads) to 6 %
 // (D = 64: 338 -> 358 us at 8,192 causal, 16/4 heads).
 constexpr float kDominant = 64.f;
 constexpr int kSample = 8;  // steps of which one is looked at

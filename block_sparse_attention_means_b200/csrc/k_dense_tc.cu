@@ -17,7 +17,9 @@
 // its O.  It does so only when its running maximum grows by more than 2^8 (P stays
 // below 2^8, exact in the end since O and l carry the same reference).
 //
-// P is rounded to bf16 (the MMA's operand type), l sums the unrounded values.
+// P is rounded to bf16, the only operand type beside V's; l sums the unrounded values.  Each rounding is off by 1.7e-3 at root
+// mean square, so o, a weighted sum of many, is 1.2e-3 to 1.7e-3 of its norm off before its own rounding of 1.65e-3: 2.0e-3 to
+// 2.3e-3 measured.  A second bf16 part of P would double the products with V, half of this kernel's.
 //
 // Warps 0-7: Softmax (stage = warp / 4) and epilogue; 8: TMA; 9: MMA; 10: forwards the V
 // tiles to the MMA warp and, in tiles that a mask cuts, replaces infinities and NaN by 0:
@@ -66,7 +68,6 @@ struct FwdSmem {
 // pair in four moved 1248 / 814, with three in eight 1203 / 830.
 __device__ constexpr bool poly_pair(int e) { return e % 4 == 0; }
 
-// The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
 // Row of a group's rows -> token (a division only where heads share keys).
 __device__ __forceinline__ int token_of(int r, int G) { return G == 1 ? r : r / G; }
 
@@ -94,6 +95,7 @@ struct RowWalk {
     }
 };
 
+// The CTA's piece: rows r0 .. of the sequence's nq G rows, key tiles j_lo .. j_lo + nt[t] - 1 of stage t.
 template <int NS>
 struct Piece {
     int r0, rows, nt[NS], j_lo, jmax;

@@ -3,7 +3,9 @@ width), the RMS norm of queries and keys for each head with the rotation in the
 same pass, and dense attention over whole prompts, each with its gradient.
 
 Thin binding like park.py: torch supplies device memory and streams, every step
-runs in the library's CUDA kernels.  Tensors are [B, H, N, D] on one CUDA device
+runs in the library's CUDA kernels.  Nothing here is recorded by autograd: results
+carry no graph, also from inputs that require gradients, which come from the
+..._bwd calls (in a torch.autograd.Function, say).  Tensors are [B, H, N, D] on one CUDA device
 in torch.bfloat16 or torch.float32, D a multiple of 32 up to 128, the last axis
 contiguous; the other strides are free as long as rows start on 16 bytes, so the
 parts of a fused projection [B, N, 3, H, D] are passed as views.
@@ -465,7 +467,8 @@ def attention(Q, K, V, causal: bool = False, scale: float | None = None, cu_q=No
 
 def attention_bwd(dO, Q, K, V, O, lse, causal: bool = False, scale: float | None = None, cu_q=None, cu_k=None, dQ=None,
                   dK=None, dV=None, ws=None, status=None, stream=None):
-    """(dQ, dK, dV) from dO and from attention's inputs and results; dK and dV are sums
+    """(dQ, dK, dV) from dO and from attention's inputs and results, O and lse of one call
+    over all of a row's keys (not joined from calls over parts of them); dK and dV are sums
     over the query heads that share a key head.  Rows outside the packed sequences are
     not written (in new tensors they are undefined)."""
     index = _attn_check(Q, K, V)

@@ -323,8 +323,8 @@ int park_qk_norm_rope_bwd(const park_operand *dq_out, const park_operand *dk_out
  *               Nk key rows; cu_q, cu_k unused.
  *   n_seq  > 0: packed (B == 1): sequence s has query rows cu_q[s] .. cu_q[s+1]-1 of
  *               Nq and key rows cu_k[s] .. cu_k[s+1]-1 of Nk; cu_q, cu_k are device
- *               int32 [n_seq + 1], rising.  Empty sequences are allowed, rows outside
- *               every sequence are neither read nor written.  A sequence whose bounds
+ *               int32 [n_seq + 1], rising.  Empty sequences are allowed; rows outside
+ *               every sequence are not written, and what they hold does not matter.  A sequence whose bounds
  *               are not 0 <= cu[s] <= cu[s+1] <= N sets *status to PARK_ERR_INDEX and is
  *               skipped.
  *   scale:      positive and finite.
@@ -333,9 +333,12 @@ int park_qk_norm_rope_bwd(const park_operand *dq_out, const park_operand *dk_out
  *   heads:      Q and O have Hq heads, K and V Hk; Hk divides Hq and query head h reads
  *               key head h / (Hq / Hk).
  * What a mask hides does not reach a row: keys and values behind it may hold
- * infinities or NaN.  Sums are float32; bf16 probabilities round once before their
- * product with v (and, in the gradients, the probabilities and the gradients of the
- * scores before theirs).  Every sum runs in a fixed order. */
+ * infinities or NaN.  Sums are float32.  With bf16 tensors the probabilities (whose
+ * exponentials are good to 2^-18) round to bf16 before their product with v, and in the
+ * gradients the probabilities and the gradients of the scores before theirs, the operand
+ * type of the tensor cores: on random inputs o is 2.0e-3 of its norm off, where the
+ * rounding of o itself is 1.65e-3.  float32 tensors keep float32 throughout.  Every sum runs in a
+ * fixed order. */
 typedef struct {
     int B, D, dtype;
     int64_t Nq, Nk;
@@ -353,9 +356,11 @@ int park_attention_workspace(const park_attn_shape *shape, int Hq, int Hk, int b
 int park_attention(const park_attn_shape *shape, const park_operand *q, const park_operand *k, const park_operand *v,
                    const park_operand *o, float *lse, void *ws, size_t ws_bytes, int32_t *status, void *stream);
 
-/* Gradients from o and lse of park_attention and the gradient of o.  dk, dv are sums
- * over the query heads that share a key head.  Rows outside every sequence are left
- * as they were. */
+/* Gradients from o and lse of park_attention and the gradient of o.  o and lse have to
+ * be those of these queries over these keys, all of them: the gradients of a row's scores
+ * are taken to sum to 0, which those of a part of a longer row's keys do not.  There
+ * is no gradient of lse.  dk, dv are sums over the query heads that share a key head.
+ * Rows outside every sequence are left as they were. */
 int park_attention_bwd(const park_attn_shape *shape, const park_operand *d_o, const park_operand *q,
                        const park_operand *k, const park_operand *v, const park_operand *o, const float *lse,
                        const park_operand *dq, const park_operand *dk, const park_operand *dv, void *ws,
