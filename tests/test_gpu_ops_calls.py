@@ -105,3 +105,64 @@ def test_the_layer_on_a_busy_stream():
         assert not side.query()
         torch.cuda.synchronize()
         assert torch.equal(got, res)
+
+
+def test_captured_layer_reports_each_replay():
+    """A captured layer(pre=...) clears and reports its status with every replay, without the default status word."""
+    B, H, T, Hg, W, text, D = 1, 2, 4, 8, 8, 16, 128
+    shape = park.Shape(B, H, T, Hg, W, text, D)
+    q, k, v = (rand(730 + i, B, H, shape.N, D, dt=BF) for i in range(3))
+    good = grid_positions((T, Hg, W), shape.N).to(torch.int32).contiguous().cuda()
+    bad = good.clone()
+    bad[70, 2] = W
+    pos = good.clone()
+    pre = park.NormRope(rope=park.rope_table((T, Hg, W), D), positions=pos)
+    want, _ = park.layer(q, k, v, shape, 8, 8, 0.9, 3, pre=pre)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, r = park.layer(q, k, v, shape, 8, 8, 0.9, 3, pre=pre)
+    for p, code in ((good, _lib.PARK_OK), (bad, _lib.PARK_ERR_INDEX), (good, _lib.PARK_OK)):
+        pos.copy_(p)
+        graph.replay()
+        assert r.status_code() == code
+    assert torch.equal(got, want)
+
+
+def test_training_steps_and_layers_at_once():
+    """Steps in both types, graphs of them and a layer on streams of their own: the bits of each alone."""
+    n, D = 1100, 128
+    r = park.rope_table((11, 10, 10), D)
+    shape = park.Shape(1, 4, 11, 10, 10, 0, D)
+    w = torch.ones(D, device="cuda")
+
+    def step(x):
+        a, b = park.qk_norm_rope(x[0], x[1], w, w, rope=r)
+        o, lse = park.attention(a, b, x[2], causal=True, return_lse=True)
+        da, db, dv = park.attention_bwd(x[3], a, b, x[2], o, lse, causal=True)
+        return (o, dv, *park.qk_norm_rope_bwd(da, db, x[0], x[1], w, w, rope=r))
+    jobs = []
+    for i, (dt, hq, hk) in enumerate(((BF, 4, 4), (F32, 6, 2), (BF, 20, 20), (BF, 8, 1))):
+        x = attn_inputs(1, hq, hk, n, n, D, dt, "tokens", seed=740 + 10 * i)
+        jobs.append(lambda x=x: step(x))
+    x = attn_inputs(1, 4, 4, n, n, D, BF, "heads", seed=780)[:3]
+    jobs.append(lambda: (park.layer(*x, shape, 12, 12, 0.9, 3, pre=park.NormRope(rope=r))[0],))
+    want = [[t.clone() for t in job()] for job in jobs]
+    graphs = []
+    for job in jobs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = job()
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream() for _ in range(len(jobs) + len(graphs))]
+    for _ in range(4):
+        torch.cuda.synchronize()
+        got = []
+        for job, s in zip(jobs, streams):
+            with torch.cuda.stream(s):
+                got.append(job())
+        for (g, _), s in zip(graphs, streams[len(jobs):]):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got + [out for _, out in graphs], want + want[:2]):
+            assert all(torch.equal(u, t) for u, t in zip(a, b))

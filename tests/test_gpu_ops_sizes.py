@@ -141,3 +141,31 @@ def test_float32_single_rows_over_long_keys(G, D):
     lk = [20000, 1, 7777, 257]
     q, k, v, do = attn_inputs(1, 2 * G, 2, len(lk), sum(lk), D, F32, "tokens", seed=600)
     check_attention(16, q, k, v, do, F32, causal=True, cu_q=cu_of([1] * len(lk)), cu_k=cu_of(lk))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_hidden_rows_in_large_blocks(dt, bad, D):
+    """Keys, values, queries and gradients behind the mask hold NaN or infinities (blocks of 256 rows, 128 in float32)."""
+    n, at, H, Hk = 600, 405, 40, 20
+    q, k, v, do = attn_inputs(1, H, Hk, n, n, D, dt, "tokens")
+    good, glse = park.attention(q, k, v, causal=True, return_lse=True)
+    ggrads = park.attention_bwd(do, q, k, v, good, glse, causal=True)
+    k2, v2 = k.clone(), v.clone()
+    v2[:, :, at, 3:9] = bad                          # rows before `at` do not see it
+    k2[:, :, at] = bad
+    o, lse = park.attention(q, k2, v2, causal=True, return_lse=True)
+    assert torch.equal(o[:, :, :at], good[:, :, :at]) and torch.equal(lse[:, :, :at], glse[:, :, :at])
+    grads = park.attention_bwd(do, q, k2, v2, o, lse, causal=True)
+    assert torch.equal(grads[0][:, :, :at], ggrads[0][:, :, :at])
+    o, _ = park.attention(q, k, v2, causal=True, return_lse=True)
+    assert torch.equal(o[:, :, :at], good[:, :, :at]) and not o[:, :, at:, 3:9].isfinite().any()
+    assert torch.equal(o[:, :, at:, 9:], good[:, :, at:, 9:]) and torch.equal(o[:, :, at:, :3], good[:, :, at:, :3])
+    q2, do2 = q.clone(), do.clone()
+    q2[:, :, at - 200] = bad
+    do2[:, :, at - 200, 5] = bad
+    o, lse = park.attention(q2, k, v, causal=True, return_lse=True)
+    grads = park.attention_bwd(do2, q2, k, v, o, lse, causal=True)
+    for i in (1, 2):
+        assert torch.equal(grads[i][:, :, at - 199:], ggrads[i][:, :, at - 199:])
