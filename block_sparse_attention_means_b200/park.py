@@ -15,6 +15,7 @@ import dataclasses
 import torch
 
 from . import _lib
+from .ops import _On
 
 _DT = {torch.bfloat16: _lib.PARK_BF16, torch.float32: _lib.PARK_F32}
 
@@ -139,30 +140,31 @@ def _check_inputs(shape: Shape, *ts):
         if tuple(t.shape) != want or t.dtype != shape.dtype or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"expected contiguous CUDA {shape.dtype} tensor of shape {want}, got "
                              f"{tuple(t.shape)} {t.dtype} contiguous={t.is_contiguous()} device={t.device}")
+        if t.device != ts[0].device:
+            raise ValueError(f"tensors on {ts[0].device} and on {t.device}")
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _outputs(shape: Shape, NQ: int, NK: int, Q, r: Retrieval | None, ws):
+    """(r, ws) on Q's device, allocated where the caller passes none."""
+    r = r or alloc_retrieval(shape, NQ, NK, Q.device)
+    ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
+    if r.status.device != Q.device or ws.device != Q.device:
+        raise ValueError(f"tensors on {Q.device}, the retrieval on {r.status.device}, the workspace on {ws.device}")
+    return r, ws
 
 
-def _allocating_on(stream):
-    """What a call allocates (workspace, outputs and their zeros) belongs to the stream that it
-    runs on: the memory of a workspace that is dropped on return is then not handed out while
-    the call's kernels still use it.  None: the current stream."""
-    return torch.cuda.stream(stream)
-
-
+# The three calls run on the tensors' device and the given (or its current) stream, and what they allocate (workspace,
+# outputs and their zeros) belongs to that stream: the memory of a workspace that is dropped on return is not handed out
+# while the call's kernels still use it.
 def retrieve(Q, K, shape: Shape, NQ: int, NK: int, p: float, iters: int, out: Retrieval | None = None,
              ws: torch.Tensor | None = None, stream=None) -> Retrieval:
     _check_inputs(shape, Q, K)
-    with _allocating_on(stream):
-        out = out or alloc_retrieval(shape, NQ, NK, Q.device)
-        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
-    s, r = shape.c(), out.c()
-    rc = _lib.load().park_retrieve(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()), ctypes.byref(s),
-                                   NQ, NK, float(p), int(iters), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
-                                   ws.numel(), _stream(stream))
+    with _On(Q.get_device(), stream) as st:
+        out, ws = _outputs(shape, NQ, NK, Q, out, ws)
+        s, r = shape.c(), out.c()
+        rc = _lib.load().park_retrieve(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()), ctypes.byref(s),
+                                       NQ, NK, float(p), int(iters), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
+                                       ws.numel(), ctypes.c_void_p(st))
     _lib.check(rc, "park_retrieve")
     return out
 
@@ -170,15 +172,15 @@ def retrieve(Q, K, shape: Shape, NQ: int, NK: int, p: float, iters: int, out: Re
 def sparse_attn(Q, K, V, shape: Shape, NQ: int, NK: int, r: Retrieval, O: torch.Tensor | None = None,
                 ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _check_inputs(shape, Q, K, V)
-    with _allocating_on(stream):
+    with _On(Q.get_device(), stream) as st:
         O = O if O is not None else torch.empty_like(Q)
-        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
-    _check_inputs(shape, O)
-    s, rc_ = shape.c(), r.c()
-    rc = _lib.load().park_sparse_attn(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
-                                      ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, ctypes.byref(rc_),
-                                      ctypes.c_void_p(O.data_ptr()), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-                                      _stream(stream))
+        _check_inputs(shape, Q, O)
+        r, ws = _outputs(shape, NQ, NK, Q, r, ws)
+        s, rc_ = shape.c(), r.c()
+        rc = _lib.load().park_sparse_attn(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
+                                          ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, ctypes.byref(rc_),
+                                          ctypes.c_void_p(O.data_ptr()), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+                                          ctypes.c_void_p(st))
     _lib.check(rc, "park_sparse_attn")
     return O
 
@@ -193,22 +195,21 @@ def layer(Q, K, V, shape: Shape, NQ: int, NK: int, p: float, iters: int, O: torc
     if pre is not None:
         if not Q.is_cuda:
             raise ValueError(f"Q: expected a CUDA tensor, got one on {Q.device}")
-        with _allocating_on(stream):
+        with _On(Q.get_device(), stream):
             met = torch.zeros(1, dtype=torch.int32, device=Q.device)
         Q, K = pre(Q, K, status=met, stream=stream)
     _check_inputs(shape, Q, K, V)
-    with _allocating_on(stream):
+    with _On(Q.get_device(), stream) as st:
         O = O if O is not None else torch.empty_like(Q)
-        out = out or alloc_retrieval(shape, NQ, NK, Q.device)
-        ws = ws if ws is not None else alloc_workspace(shape, NQ, NK, Q.device)
-    s, r = shape.c(), out.c()
-    rc = _lib.load().park_layer(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
-                                ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, float(p), int(iters),
-                                ctypes.c_void_p(O.data_ptr()), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
-                                ws.numel(), _stream(stream))
-    _lib.check(rc, "park_layer")
-    if met is not None:  # (retrieval clears the status word first, so what pre met is added last)
-        with _allocating_on(stream):
+        _check_inputs(shape, Q, O)
+        out, ws = _outputs(shape, NQ, NK, Q, out, ws)
+        s, r = shape.c(), out.c()
+        rc = _lib.load().park_layer(ctypes.c_void_p(Q.data_ptr()), ctypes.c_void_p(K.data_ptr()),
+                                    ctypes.c_void_p(V.data_ptr()), ctypes.byref(s), NQ, NK, float(p), int(iters),
+                                    ctypes.c_void_p(O.data_ptr()), ctypes.byref(r), ctypes.c_void_p(ws.data_ptr()),
+                                    ws.numel(), ctypes.c_void_p(st))
+        _lib.check(rc, "park_layer")
+        if met is not None:  # (retrieval clears the status word first, so what pre met is added last)
             torch.where(out.status == 0, met, out.status, out=out.status)
     return O, out
 

@@ -3,6 +3,7 @@ argument is answered on the host, before anything is enqueued."""
 import copy
 import ctypes
 import pickle
+import types
 
 import pytest
 import torch
@@ -277,3 +278,54 @@ def test_single_rows_split_their_keys_into_whole_waves(dt, waves, hq, hk, nk):
     tile = 128 if dt == _lib.PARK_BF16 else 64
     least = min(waves * 148, (nk + tile - 1) // tile * hk / 4)   # (parts of a few tiles at least)
     assert least / 1.5 - hk <= parts * hk <= waves * 148 + (hk if dt == _lib.PARK_F32 else 0)
+
+
+def stand_in(index, shape=(1, 2, 40, 64), dtype=torch.bfloat16):
+    """What the layer's calls look at of a tensor on another device."""
+    return types.SimpleNamespace(shape=shape, dtype=dtype, is_contiguous=lambda: True, is_cuda=True,
+                                 device=torch.device("cuda", index), get_device=lambda: index, data_ptr=lambda: FAKE,
+                                 numel=lambda: 1 << 30)
+
+
+def test_the_layer_runs_on_its_tensors_device_and_stream(monkeypatch):
+    from block_sparse_attention_means_b200 import ops
+    seen, here = [], [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            here.append(self.index)
+
+        def __exit__(self, *exc):
+            here.pop()
+    lib = types.SimpleNamespace(**{n: lambda *a, n=n: seen.append((n, here[-1], a[-1].value)) or 0
+                                   for n in ("park_retrieve", "park_sparse_attn", "park_layer")})
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: here[-1])
+    monkeypatch.setattr(ops, "_raw_stream", lambda index: 1000 * index)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    shape = park.Shape(1, 2, 2, 4, 5, 0, 64)
+    r = types.SimpleNamespace(status=stand_in(1), c=_lib.ParkRetrieval)
+    q, ws = stand_in(1), stand_in(1)
+    park.retrieve(q, q, shape, 4, 4, 0.9, 3, out=r, ws=ws)
+    park.sparse_attn(q, q, q, shape, 4, 4, r, O=stand_in(1), ws=ws)
+    park.layer(q, q, q, shape, 4, 4, 0.9, 3, O=stand_in(1), out=r, ws=ws)
+    assert seen == [(n, 1, 1000) for n in ("park_retrieve", "park_sparse_attn", "park_layer")] and here == [0]
+    # tensors, results or a stream of different devices
+    host = stand_in(0)
+    host.device = torch.device("cpu")
+    with pytest.raises(ValueError):
+        park.retrieve(q, stand_in(0), shape, 4, 4, 0.9, 3, out=r, ws=ws)
+    with pytest.raises(ValueError):
+        park.layer(q, q, q, shape, 4, 4, 0.9, 3, O=stand_in(0), out=r, ws=ws)
+    with pytest.raises(ValueError):
+        park.layer(q, q, q, shape, 4, 4, 0.9, 3, O=stand_in(1, (1, 2, 39, 64)), out=r, ws=ws)
+    with pytest.raises(ValueError):
+        park.layer(q, q, q, shape, 4, 4, 0.9, 3, O=stand_in(1), out=r, ws=host)
+    with pytest.raises(ValueError):
+        park.layer(q, q, q, shape, 4, 4, 0.9, 3, O=stand_in(1), out=types.SimpleNamespace(status=stand_in(0)), ws=ws)
+    with pytest.raises(ValueError):
+        park.retrieve(q, q, shape, 4, 4, 0.9, 3, out=r, ws=ws, stream=types.SimpleNamespace(device=stand_in(0).device))
+    assert len(seen) == 3
