@@ -98,7 +98,7 @@ def test_the_layer_on_a_busy_stream():
         torch.cuda.synchronize()
         torch.cuda.empty_cache()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(200_000_000)               # about 0.1 s
+            torch.cuda._sleep(800_000_000)               # about 0.4 s
         got = call()
         over = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(3)]
         over += [torch.full_like(t, 7.0) for t in (q, k, q, k)]
